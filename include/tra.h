@@ -76,7 +76,7 @@ typedef enum {
     TRA_OK = 0,
     TRA_ERR_INVALID_ARG = 1,   /* bad argument: null/misaligned pointer, bad size */
     TRA_ERR_UNSUPPORTED = 2,   /* valid but outside what the kernels support */
-    TRA_ERR_WORKSPACE = 3,     /* mask buffer smaller than tra_plan_info.mask_bytes */
+    TRA_ERR_WORKSPACE = 3,     /* a mask or workspace buffer smaller than its required size */
     TRA_ERR_CUDA = 4,          /* a CUDA runtime/driver call or launch failed */
     TRA_ERR_TIMEOUT = 5,       /* a kernel's bounded wait gave up (device side) */
     TRA_ERR_DEVICE_CHECK = 6   /* a kernel's own index check failed (device side) */
@@ -248,6 +248,54 @@ TRA_API tra_status tra_radius_and_mask(tra_plan plan, const float* Hent, void* m
  */
 TRA_API tra_status tra_attention(tra_plan plan, const void* q, const void* k, const void* v,
                          const void* mask, void* out, tra_stream stream);
+
+/*
+ * tra_attention_lse -- tra_attention that also writes each row's log-sum-exp,
+ *   lse_i = ln sum_{j in M_i} exp(q_i.k_j / sqrt d),
+ * which tra_attention_backward needs, and with which partial results over
+ * disjoint key sets are merged.  O is normalised by the sum of the unrounded
+ * P (tra_attention: by the sum of the bf16-rounded P), so the two outputs may
+ * differ by the rounding of P.
+ *   q, k, v, mask, out   as tra_attention
+ *   lse   device fp32 [heads][N_pad] ([heads][N] with TRA_FLAG_NATURAL); pad
+ *         rows unspecified
+ * Asynchronous on `stream`.
+ */
+TRA_API tra_status tra_attention_lse(tra_plan plan, const void* q, const void* k, const void* v,
+                         const void* mask, void* out, float* lse, tra_stream stream);
+
+/*
+ * tra_attention_backward -- the gradients of tra_attention_lse's `out` under
+ * the same mask, the probabilities recomputed from lse.  With
+ * P_ij = exp(q_i.k_j / sqrt d - lse_i) over the kept pairs and
+ * dS_ij = P_ij (dO_i.v_j - dO_i.O_i):
+ *   dV_j = sum_i P_ij dO_i,  dK_j = sum_i dS_ij q_i / sqrt d,
+ *   dQ_i = sum_j dS_ij k_j / sqrt d.
+ * The radii are constants of the mask: no gradient flows through them.  The
+ * products run on the tensor cores with fp32 accumulation; P, dS and, when it
+ * is fp32, dO are rounded to bf16.  Results are bit-identical from run to run.
+ *   q, k, v, mask   as tra_attention
+ *   out, lse        what tra_attention_lse wrote for them
+ *   dout            the gradient of out, in out's type and layout, finite; pad
+ *                   rows are not read
+ *   dq, dk, dv      device, in out's type and layout; pad rows of the
+ *                   tile-major layout get zeros.  They may not overlap an
+ *                   input.
+ *   workspace       device, 256-byte aligned, at least
+ *                   tra_attention_backward_bytes; contents need not be kept
+ *                   between calls, but calls that may run at the same time
+ *                   need one each
+ * Errors in the mask buffer are recorded as by tra_attention.
+ * TRA_ERR_WORKSPACE when workspace_bytes is too small.  Asynchronous on
+ * `stream`.
+ */
+TRA_API tra_status tra_attention_backward(tra_plan plan, const void* q, const void* k, const void* v,
+                         const void* mask, const void* out, const float* lse, const void* dout,
+                         void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                         tra_stream stream);
+
+/* the workspace size of tra_attention_backward; no CUDA call */
+TRA_API tra_status tra_attention_backward_bytes(tra_plan plan, size_t* bytes);
 
 /*
  * tra_calibrate_topk -- calibration workload (the summary's Intuition I: the

@@ -20,7 +20,8 @@ from dataclasses import dataclass
 __all__ = [
     "TraError", "PlanInfo", "Plan", "library_path", "load_library",
     "tra_plan_create", "tra_plan_destroy", "tra_plan_query", "tra_permute", "tra_entropy",
-    "tra_radius_and_mask", "tra_attention", "tra_calibrate_topk", "tra_calibrate_fit", "tra_plan_status",
+    "tra_radius_and_mask", "tra_attention", "tra_attention_lse", "tra_attention_backward",
+    "tra_attention_backward_bytes", "tra_calibrate_topk", "tra_calibrate_fit", "tra_plan_status",
     "tra_status_string",
     "TRA_FLAG_DEBUG_NO_WAIT", "TRA_FLAG_OUT_BF16", "TRA_FLAG_NATURAL", "TRA_FLAG_DISK", "TRA_FLAG_QSORT",
     "tra_flag_tile_w",
@@ -112,6 +113,12 @@ def load_library() -> ctypes.CDLL:
     L.tra_radius_and_mask.restype = st
     L.tra_attention.argtypes = [vp, vp, vp, vp, vp, vp, vp]
     L.tra_attention.restype = st
+    L.tra_attention_lse.argtypes = [vp] * 8
+    L.tra_attention_lse.restype = st
+    L.tra_attention_backward.argtypes = [vp] * 12 + [ctypes.c_size_t, vp]
+    L.tra_attention_backward.restype = st
+    L.tra_attention_backward_bytes.argtypes = [vp, ctypes.POINTER(ctypes.c_size_t)]
+    L.tra_attention_backward_bytes.restype = st
     L.tra_calibrate_topk.argtypes = [vp, vp, vp, ctypes.c_double, i, vp, vp, vp]
     L.tra_calibrate_topk.restype = st
     L.tra_calibrate_fit.argtypes = [vp, vp, ctypes.c_longlong, ctypes.POINTER(ctypes.c_double),
@@ -169,6 +176,24 @@ def tra_radius_and_mask(plan, H_ptr, mask_ptr, mask_bytes, stream=0) -> None:
 
 def tra_attention(plan, q_ptr, k_ptr, v_ptr, mask_ptr, out_ptr, stream=0) -> None:
     _check("tra_attention", load_library().tra_attention(plan, q_ptr, k_ptr, v_ptr, mask_ptr, out_ptr, stream))
+
+
+def tra_attention_lse(plan, q_ptr, k_ptr, v_ptr, mask_ptr, out_ptr, lse_ptr, stream=0) -> None:
+    _check("tra_attention_lse", load_library().tra_attention_lse(plan, q_ptr, k_ptr, v_ptr, mask_ptr, out_ptr,
+                                                                 lse_ptr, stream))
+
+
+def tra_attention_backward(plan, q_ptr, k_ptr, v_ptr, mask_ptr, out_ptr, lse_ptr, dout_ptr, dq_ptr, dk_ptr, dv_ptr,
+                           workspace_ptr, workspace_bytes, stream=0) -> None:
+    _check("tra_attention_backward", load_library().tra_attention_backward(
+        plan, q_ptr, k_ptr, v_ptr, mask_ptr, out_ptr, lse_ptr, dout_ptr, dq_ptr, dk_ptr, dv_ptr, workspace_ptr,
+        int(workspace_bytes), stream))
+
+
+def tra_attention_backward_bytes(plan) -> int:
+    n = ctypes.c_size_t()
+    _check("tra_attention_backward_bytes", load_library().tra_attention_backward_bytes(plan, ctypes.byref(n)))
+    return n.value
 
 
 def tra_calibrate_topk(plan, q_ptr, k_ptr, mass, query_tile_stride, H_ptr, k_out_ptr, stream=0) -> None:
@@ -257,6 +282,13 @@ class Plan:
         import torch
         return torch.empty(self.info.heads, self.io_rows, dtype=torch.float32, device=device)
 
+    def new_lse(self, device="cuda"):
+        return self.new_entropy(device)
+
+    def new_backward_workspace(self, device="cuda"):
+        import torch
+        return torch.empty(tra_attention_backward_bytes(self.handle), dtype=torch.uint8, device=device)
+
     def new_mask(self, device="cuda"):
         import torch
         return torch.empty(self.info.mask_bytes, dtype=torch.uint8, device=device)
@@ -329,6 +361,52 @@ class Plan:
         tra_attention(self.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), mask.data_ptr(), out.data_ptr(),
                       self._stream(stream))
         return out
+
+    def _buffer(self, x, dtype, numel, name):
+        """A contiguous cuda tensor of `dtype` with `numel` elements (at least, for a byte buffer)."""
+        import torch
+        enough = x.numel() >= numel if dtype == torch.uint8 else x.numel() == numel
+        if x.dtype != dtype or not x.is_cuda or not x.is_contiguous() or not enough:
+            raise ValueError(f"{name}: expected contiguous cuda {dtype} with {numel} elements, "
+                             f"got {x.dtype} {tuple(x.shape)} on {x.device}")
+
+    def _on_device(self, *tensors):
+        """All tensors on one device, which has to be the current one: the launch goes to its stream."""
+        import torch
+        if len({x.device for x in tensors}) != 1 or tensors[0].device.index != torch.cuda.current_device():
+            raise ValueError(f"tensors on {sorted({str(x.device) for x in tensors})}; expected all on the current "
+                             f"device, cuda:{torch.cuda.current_device()}")
+
+    def attention_lse(self, q, k, v, mask, out, lse, stream=None):
+        """tra_attention_lse: out and the rows' log-sum-exp (natural log)."""
+        import torch
+        i = self.info
+        for x, nme in ((q, "q"), (k, "k"), (v, "v")):
+            self._rows(x, self.io_rows, nme)
+        self._rows(out, self.io_rows, "out", self.out_dtype)
+        self._buffer(lse, torch.float32, i.heads * self.io_rows, "lse")
+        self._buffer(mask, torch.uint8, i.mask_bytes, "mask")
+        self._on_device(q, k, v, mask, out, lse)
+        tra_attention_lse(self.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), mask.data_ptr(), out.data_ptr(),
+                          lse.data_ptr(), self._stream(stream))
+        return out, lse
+
+    def attention_backward(self, q, k, v, mask, out, lse, dout, dq, dk, dv, workspace, stream=None):
+        """tra_attention_backward: the gradients of attention_lse's out, in out's type and layout."""
+        import torch
+        i = self.info
+        for x, nme in ((q, "q"), (k, "k"), (v, "v")):
+            self._rows(x, self.io_rows, nme)
+        for x, nme in ((out, "out"), (dout, "dout"), (dq, "dq"), (dk, "dk"), (dv, "dv")):
+            self._rows(x, self.io_rows, nme, self.out_dtype)
+        self._buffer(lse, torch.float32, i.heads * self.io_rows, "lse")
+        self._buffer(mask, torch.uint8, i.mask_bytes, "mask")
+        self._buffer(workspace, torch.uint8, 1, "workspace")
+        self._on_device(q, k, v, mask, out, lse, dout, dq, dk, dv, workspace)
+        tra_attention_backward(self.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), mask.data_ptr(),
+                               out.data_ptr(), lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                               dv.data_ptr(), workspace.data_ptr(), workspace.numel(), self._stream(stream))
+        return dq, dk, dv
 
     def calibrate_topk(self, q, k, mass, query_tile_stride=1, stream=None):
         """Calibration workload: (H [heads, n_sample, 128] fp32, k [heads,

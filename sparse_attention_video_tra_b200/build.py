@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libtra_b200.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
-SOURCES = ["tra_api.cu", "tra_plan.cpp"]
+SOURCES = ["tra_api.cu", "tra_grad.cu", "tra_plan.cpp"]
 
 
 def _inputs():
@@ -37,14 +37,31 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-lineinfo", "-O3", "-std=c++17", "-shared",
-           "-Xcompiler", "-fPIC,-ffp-contract=off,-fvisibility=hidden",
-           "-I", os.path.join(ROOT, "include"),
-           "-cudart", "static", "-o", tmp] + [os.path.join(CSRC, s) for s in SOURCES]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    flags = [*ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC,-ffp-contract=off,-fvisibility=hidden",
+             "-I", os.path.join(ROOT, "include")]
+    # one nvcc per source, all at once, then the link
+    objs = [f"{tmp}.{s}.o" for s in SOURCES]
+    cmds = [[nvcc, *flags, "-c", "-o", o, os.path.join(CSRC, s)] for s, o in zip(SOURCES, objs)]
+    link = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
+    try:
+        running = []
+        for cmd in cmds:
+            if verbose:
+                print(" ".join(cmd))
+            running.append(subprocess.Popen(cmd))
+        for proc, cmd in zip(running, cmds):
+            if proc.wait():
+                for other in running:
+                    other.wait()
+                raise subprocess.CalledProcessError(proc.returncode, cmd)
+        if verbose:
+            print(" ".join(link))
+        subprocess.run(link, check=True)
+        os.replace(tmp, LIB)
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
     return LIB
 
 

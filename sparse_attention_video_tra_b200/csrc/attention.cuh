@@ -105,11 +105,13 @@ __device__ __forceinline__ uint32_t pack_tile(int t, int tr, int tc)
 }
 constexpr uint32_t MT_IN0 = 1u << 26, MT_FULL0 = 1u << 28;
 
-template <int D, int TWL, bool OUT_BF16, bool DISK>
+// LSE: also write each row's log-sum-exp (natural log) to `lse`; O is then
+// normalised by the sum of the unrounded P, which is the sum the log is of.
+template <int D, int TWL, bool OUT_BF16, bool DISK, bool LSE>
 __global__ void __launch_bounds__(384, 1)
 attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const Geom G, const uint8_t* __restrict__ mask,
-                 void* __restrict__ out, const void* __restrict__ qraw)
+                 void* __restrict__ out, const void* __restrict__ qraw, float* __restrict__ lse)
 {
     using C = AttnCfg<D>;
     constexpr int TW = 1 << TWL;
@@ -651,9 +653,13 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 for (int q = 0; q < 16; ++q) {
                     float x0, x1;
                     f2_unpack(x[c * 16 + q], x0, x1);
-                    pk[q] = pack_bf16x2(ex2(x0), ex2(x1));
-                    // the row sum adds exactly the bf16 values the tensor core will use
-                    ls[q & 3] = f2_add(ls[q & 3], f2_pack(__uint_as_float(pk[q] << 16), __uint_as_float(pk[q] & 0xffff0000u)));
+                    const float p0 = ex2(x0), p1 = ex2(x1);
+                    pk[q] = pack_bf16x2(p0, p1);
+                    // the row sum adds exactly the bf16 values the tensor core will
+                    // use; with LSE the unrounded ones (the rounding of P would
+                    // show in the log: about 1e-4 of a row sum over tens of keys)
+                    ls[q & 3] = f2_add(ls[q & 3], LSE ? f2_pack(p0, p1)
+                                                      : f2_pack(__uint_as_float(pk[q] << 16), __uint_as_float(pk[q] & 0xffff0000u)));
                 }
                 tmem_st16(tmem + lane_base + colS + c * 16, pk);
             }
@@ -688,6 +694,9 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 const bool store = !G.natural || qvalid;          // natural layout has no pad rows
                 const size_t orow = io_row(G, g, tq, hq, wq, qt * 128 + qrow) * D;
+                if constexpr (LSE) {
+                    if (store) lse[orow / D] = l > 0.f ? (m_run + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                }
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t v[32];

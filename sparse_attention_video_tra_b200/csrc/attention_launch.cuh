@@ -1,0 +1,58 @@
+// attention_launch.cuh -- launches of the attention kernel: the instance by
+// (head dim, tile width, output type, spatial metric), with or without the
+// rows' log-sum-exp.
+#pragma once
+#include "tra_host.cuh"
+#include "attention.cuh"
+
+namespace {
+
+template <int D, int TWL, bool OB, bool DISK, bool LSE>
+tra_status run_attention(const tra::Geom& G, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                         const uint8_t* mask, void* out, const void* qraw, float* lse,
+                         cudaStream_t st)
+{
+    using C = tra::AttnCfg<D>;
+    auto kern = tra::attention_kernel<D, TWL, OB, DISK, LSE>;
+    const int smem = tra::attn_smem_bytes<D>(G.list_cap, G.rte, G.tiles_per_frame);
+    if (smem > kMaxSmem) return TRA_ERR_UNSUPPORTED;
+    if (!set_smem(kern, smem)) return TRA_ERR_CUDA;
+    // two query tiles per CTA; with radius-sorted groups, the same slot of
+    // frames 2f and 2f + 1, then an odd last frame's slots two by two
+    const int ctas = G.qsort ? G.T / 2 * G.tiles_per_frame + (G.T % 2) * ((G.tiles_per_frame + 1) / 2)
+                             : (G.nQ + 1) / 2;
+    kern<<<dim3(ctas, G.G), C::THREADS, smem, st>>>(q, k, v, G, mask, out, qraw, lse);
+    return launch_status();
+}
+
+template <int D, int TWL, bool LSE>
+tra_status attention_variant(const tra::Geom& G, bool ob, bool disk, const CUtensorMap& q, const CUtensorMap& k,
+                             const CUtensorMap& v, const uint8_t* m, void* out, const void* qr, float* lse,
+                             cudaStream_t st)
+{
+    if (ob) return disk ? run_attention<D, TWL, true, true, LSE>(G, q, k, v, m, out, qr, lse, st)
+                        : run_attention<D, TWL, true, false, LSE>(G, q, k, v, m, out, qr, lse, st);
+    return disk ? run_attention<D, TWL, false, true, LSE>(G, q, k, v, m, out, qr, lse, st)
+                : run_attention<D, TWL, false, false, LSE>(G, q, k, v, m, out, qr, lse, st);
+}
+
+// kernel instance by (head dim, tile width, output type, spatial metric)
+template <bool LSE>
+tra_status dispatch_attention(const tra::Geom& G, bool ob, bool disk, const CUtensorMap& q, const CUtensorMap& k,
+                              const CUtensorMap& v, const uint8_t* m, void* out, const void* qr, float* lse,
+                             cudaStream_t st)
+{
+    switch (G.D * 100 + G.tw_log2) {
+        case 6402: return attention_variant<64, 2, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
+        case 6403: return attention_variant<64, 3, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
+        case 6404: return attention_variant<64, 4, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
+        case 6405: return attention_variant<64, 5, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
+        case 12802: return attention_variant<128, 2, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
+        case 12803: return attention_variant<128, 3, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
+        case 12804: return attention_variant<128, 4, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
+        case 12805: return attention_variant<128, 5, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
+    }
+    return TRA_ERR_UNSUPPORTED;
+}
+
+}  // namespace

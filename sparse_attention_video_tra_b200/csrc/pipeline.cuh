@@ -7,8 +7,9 @@
 namespace tra {
 
 // Per-device error word: bit 0 = a bounded wait gave up, bit 1 = an index
-// check failed.  Read and cleared by the host after a stream sync.
-__device__ unsigned int g_tra_error;
+// check failed.  Read and cleared by the host after a stream sync.  Each
+// translation unit has its own; tra_plan_status reads them all.
+static __device__ unsigned int g_tra_error;
 
 // Bounded wait that also gives up as soon as another role has aborted.  On
 // give-up it raises the CTA's abort flag and the device error word.  A zero

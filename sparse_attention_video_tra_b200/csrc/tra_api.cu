@@ -1,110 +1,14 @@
-// tra_api.cu -- the extern "C" entry points that launch the kernels: argument
+// tra_api.cu -- the extern "C" entry points of the inference path: argument
 // checks, TMA tensor maps, kernel selection by (head dim, tile width), and the
-// device error word.  All kernels are compiled into this one translation unit.
-#include <cmath>
-#include <cstdint>
-#include <mutex>
-
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
-
-#include "../../include/tra.h"
-#include "tra_plan_impl.h"
-#include "pipeline.cuh"
+// device error word.
+#include "tra_host.cuh"
 #include "permute.cuh"
 #include "radius_mask.cuh"
 #include "entropy.cuh"
-#include "attention.cuh"
+#include "attention_launch.cuh"
 #include "topk.cuh"
 
 namespace {
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn()
-{
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
-// [rows][D] bf16 rows, 128-row x 64-column boxes, 128-byte swizzle
-bool make_row_map(CUtensorMap* m, const void* base, uint64_t rows, int D)
-{
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
-    const cuuint32_t box[2] = {64, 128};
-    const cuuint32_t es[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// [heads*T][H][W][D] bf16 in natural token order, {64, tw, th, 1} boxes (one
-// panel of one (1, th, tw) tile; coordinates past the grid read as zeros)
-bool make_natural_map(CUtensorMap* m, const void* base, const tra::Geom& G)
-{
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)G.D, (cuuint64_t)G.W, (cuuint64_t)G.H, (cuuint64_t)G.T * G.G};
-    const cuuint64_t strides[3] = {(cuuint64_t)G.D * 2, (cuuint64_t)G.W * G.D * 2, (cuuint64_t)G.H * G.W * G.D * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)G.tw, (cuuint32_t)G.th, 1};
-    const cuuint32_t es[4] = {1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// the input map for the plan's layout
-bool make_input_map(CUtensorMap* m, const void* base, const tra::Geom& G)
-{
-    return G.natural ? make_natural_map(m, base, G) : make_row_map(m, base, (uint64_t)G.G * G.N_pad, G.D);
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-tra_status launch_status()
-{
-    return cudaGetLastError() == cudaSuccess ? TRA_OK : TRA_ERR_CUDA;
-}
-
-template <class K>
-bool set_smem(K kernel, int bytes)
-{
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
-}
-
-// largest dynamic shared memory a CTA may use on sm_100
-constexpr int kMaxSmem = 232448;
-
-template <int D, int TWL, bool OB, bool DISK>
-tra_status run_attention(const tra::Geom& G, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                         const uint8_t* mask, void* out, const void* qraw, cudaStream_t st)
-{
-    using C = tra::AttnCfg<D>;
-    auto kern = tra::attention_kernel<D, TWL, OB, DISK>;
-    const int smem = tra::attn_smem_bytes<D>(G.list_cap, G.rte, G.tiles_per_frame);
-    if (smem > kMaxSmem) return TRA_ERR_UNSUPPORTED;
-    if (!set_smem(kern, smem)) return TRA_ERR_CUDA;
-    // two query tiles per CTA; with radius-sorted groups, the same slot of
-    // frames 2f and 2f + 1, then an odd last frame's slots two by two
-    const int ctas = G.qsort ? G.T / 2 * G.tiles_per_frame + (G.T % 2) * ((G.tiles_per_frame + 1) / 2)
-                             : (G.nQ + 1) / 2;
-    kern<<<dim3(ctas, G.G), C::THREADS, smem, st>>>(q, k, v, G, mask, out, qraw);
-    return launch_status();
-}
 
 template <int D, int TWL>
 tra_status run_entropy(const tra::Geom& G, const CUtensorMap& q, const CUtensorMap& k, int stride, float corr,
@@ -209,37 +113,6 @@ extern "C" tra_status tra_radius_and_mask(tra_plan plan, const float* Hent, void
     return launch_status();
 }
 
-namespace {
-
-template <int D, int TWL>
-tra_status attention_variant(const tra::Geom& G, bool ob, bool disk, const CUtensorMap& q, const CUtensorMap& k,
-                             const CUtensorMap& v, const uint8_t* m, void* out, const void* qr, cudaStream_t st)
-{
-    if (ob) return disk ? run_attention<D, TWL, true, true>(G, q, k, v, m, out, qr, st)
-                        : run_attention<D, TWL, true, false>(G, q, k, v, m, out, qr, st);
-    return disk ? run_attention<D, TWL, false, true>(G, q, k, v, m, out, qr, st)
-                : run_attention<D, TWL, false, false>(G, q, k, v, m, out, qr, st);
-}
-
-// kernel instance by (head dim, tile width, output type, spatial metric)
-tra_status dispatch_attention(const tra::Geom& G, bool ob, bool disk, const CUtensorMap& q, const CUtensorMap& k,
-                              const CUtensorMap& v, const uint8_t* m, void* out, const void* qr, cudaStream_t st)
-{
-    switch (G.D * 100 + G.tw_log2) {
-        case 6402: return attention_variant<64, 2>(G, ob, disk, q, k, v, m, out, qr, st);
-        case 6403: return attention_variant<64, 3>(G, ob, disk, q, k, v, m, out, qr, st);
-        case 6404: return attention_variant<64, 4>(G, ob, disk, q, k, v, m, out, qr, st);
-        case 6405: return attention_variant<64, 5>(G, ob, disk, q, k, v, m, out, qr, st);
-        case 12802: return attention_variant<128, 2>(G, ob, disk, q, k, v, m, out, qr, st);
-        case 12803: return attention_variant<128, 3>(G, ob, disk, q, k, v, m, out, qr, st);
-        case 12804: return attention_variant<128, 4>(G, ob, disk, q, k, v, m, out, qr, st);
-        case 12805: return attention_variant<128, 5>(G, ob, disk, q, k, v, m, out, qr, st);
-    }
-    return TRA_ERR_UNSUPPORTED;
-}
-
-}  // namespace
-
 extern "C" tra_status tra_attention(tra_plan plan, const void* q, const void* k, const void* v, const void* mask,
                                     void* out, tra_stream stream)
 {
@@ -254,7 +127,7 @@ extern "C" tra_status tra_attention(tra_plan plan, const void* q, const void* k,
     const uint8_t* m = (const uint8_t*)mask;
     const bool ob = (plan->flags & TRA_FLAG_OUT_BF16) != 0;
     const bool disk = G.disk != 0;
-    return dispatch_attention(G, ob, disk, mq, mk, mv, m, out, q, st);
+    return dispatch_attention<false>(G, ob, disk, mq, mk, mv, m, out, q, nullptr, st);
 }
 
 extern "C" tra_status tra_calibrate_topk(tra_plan plan, const void* q, const void* k, double mass,
@@ -286,11 +159,7 @@ extern "C" tra_status tra_plan_status(tra_plan plan)
 {
     (void)plan;
     unsigned int word = 0;
-    if (cudaMemcpyFromSymbol(&word, tra::g_tra_error, sizeof word) != cudaSuccess) return TRA_ERR_CUDA;
-    if (word) {
-        const unsigned int zero = 0;
-        if (cudaMemcpyToSymbol(tra::g_tra_error, &zero, sizeof zero) != cudaSuccess) return TRA_ERR_CUDA;
-    }
+    if (!take_error_word(word) || !tra_grad_take_error(word)) return TRA_ERR_CUDA;
     if (word & TRA_ERRBIT_TIMEOUT) return TRA_ERR_TIMEOUT;
     if (word & TRA_ERRBIT_CHECK) return TRA_ERR_DEVICE_CHECK;
     return TRA_OK;

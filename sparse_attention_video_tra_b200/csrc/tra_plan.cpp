@@ -210,7 +210,7 @@ extern "C" const char* tra_status_string(tra_status s)
         case TRA_OK: return "ok";
         case TRA_ERR_INVALID_ARG: return "invalid argument";
         case TRA_ERR_UNSUPPORTED: return "unsupported shape or parameter";
-        case TRA_ERR_WORKSPACE: return "mask buffer too small";
+        case TRA_ERR_WORKSPACE: return "mask or workspace buffer too small";
         case TRA_ERR_CUDA: return "CUDA call failed";
         case TRA_ERR_TIMEOUT: return "a kernel wait gave up (timeout)";
         case TRA_ERR_DEVICE_CHECK: return "a kernel index check failed";

@@ -11,3 +11,6 @@ struct tra_plan_s {
     unsigned flags;
     size_t mask_bytes;
 };
+
+// read and clear the error word of the other translation units' kernels
+bool tra_grad_take_error(unsigned int& word);
