@@ -224,8 +224,8 @@ def _prepare_own(s):
             view.view(torch.uint8).copy_(held.view(view.shape).view(torch.uint8))
         s["out"] = torch.empty_like(s["q"])
         s["lse"] = torch.empty(s["q"].shape[:2], device="cuda")
-        if c["op"] == "tokens":
-            s["workspace"] = plan.new_token_workspace(c["tokens"])
+        if c["op"] == "frames":
+            s["workspace"] = plan.new_cache_workspace(c["frames"])
 
 
 # ------------------------------------------------------------------ one pass
@@ -247,10 +247,9 @@ def _run_own(s):
         f = slice(c["frame"], c["frame"] + c["frames"])
         return tuple(x.unflatten(1, (c["T"], -1))[:, f] for x in plan.cache_views(s["cache"]))
     if c["op"] == "frames":
-        plan.cache_attention(s["q"], c["frame"], s["cache"], s["cached"], s["mask"], s["out"], s["lse"])
+        plan.cache_attention(s["q"], c["frame"], s["cache"], s["cached"], s["mask"], s["out"], s["lse"], s["workspace"])
     else:
-        plan.cache_attention_tokens(s["q"], s["token"], s["token_radius"], s["cache"], s["cached"], s["out"], s["lse"],
-                                    s["workspace"])
+        plan.cache_attention_tokens(s["q"], s["token"], s["token_radius"], s["cache"], s["cached"], s["out"], s["lse"])
     return s["out"], s["lse"]
 
 
