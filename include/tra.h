@@ -297,6 +297,77 @@ TRA_API tra_status tra_attention_backward(tra_plan plan, const void* q, const vo
 /* the workspace size of tra_attention_backward; no CUDA call */
 TRA_API tra_status tra_attention_backward_bytes(tra_plan plan, size_t* bytes);
 
+/* the 8-bit cache of a plan: its size and the byte offsets of its parts */
+typedef struct {
+    size_t cache_bytes;
+    /* k, v              e4m3   [heads][n_tiles][128][d] codes, tile-major rows; zeros on pad rows
+       k_scale, v_scale  fp32   [heads][n_tiles], a power of two per tile:
+                         the stored value of a row is its codes times the scale of its tile */
+    size_t off_k, off_v, off_k_scale, off_v_scale;
+} tra_cache_info;
+
+/* copy the sizes of the plan's cache into *info; no CUDA call */
+TRA_API tra_status tra_cache_query(tra_plan plan, tra_cache_info* info);
+
+/*
+ * tra_cache_store -- frames of keys and values into the 8-bit cache.  Each
+ * (head, tile) of a stored frame gets the scale 2^e with the smallest
+ * e >= -126 that brings the tile's largest magnitude to at most 448 (2^0 for a
+ * tile of zeros), and the codes rn(x / 2^e) in e4m3.  Tiles lie in one frame:
+ * the other frames of the cache stay as they were, and storing a frame again
+ * replaces it.
+ *   k, v      device bf16, the rows of the frames [frame, frame + n_frames)
+ *             only: [heads][n_frames * n_tiles_h * n_tiles_w * 128][d]
+ *             tile-major, [heads][n_frames * H * W][d] with TRA_FLAG_NATURAL;
+ *             16-byte aligned, finite (pad rows are not read)
+ *   cache     device, 256-byte aligned, at least cache_bytes (tra_cache_query)
+ * TRA_ERR_INVALID_ARG for frames outside the grid.  Asynchronous on `stream`.
+ */
+TRA_API tra_status tra_cache_store(tra_plan plan, const void* k, const void* v, int frame, int n_frames,
+                         void* cache, size_t cache_bytes, tra_stream stream);
+
+/*
+ * tra_cache_attention -- tra_attention_lse of the queries of some frames over
+ * the frames that the cache holds so far: the keys of query i are those of M_i
+ * in the frames [0, cached_frames).
+ *   q, out, lse    the rows of the frames [frame, frame + n_frames) only, in
+ *                  the layout tra_cache_store gives for k and v (lse: one
+ *                  fp32 per row); out fp32, or bf16 with TRA_FLAG_OUT_BF16.  A
+ *                  query that keeps no cached key gets zeros and -infinity.
+ *   cache          cached frames as written by tra_cache_store; frames from
+ *                  cached_frames on are not read
+ *   mask           the mask buffer of the whole grid (only the query frames'
+ *                  part is read)
+ *   workspace      device, 256-byte aligned, at least
+ *                  tra_cache_attention_bytes; calls that may run at the same
+ *                  time need one each
+ * Asynchronous on `stream`.
+ */
+TRA_API tra_status tra_cache_attention(tra_plan plan, const void* q, int frame, int n_frames, const void* cache,
+                         size_t cache_bytes, int cached_frames, const void* mask, void* out, float* lse,
+                         void* workspace, size_t workspace_bytes, tra_stream stream);
+
+/* the workspace size of tra_cache_attention for n_frames query frames; no CUDA call */
+TRA_API tra_status tra_cache_attention_bytes(tra_plan plan, int n_frames, size_t* bytes);
+
+/*
+ * tra_cache_attention_tokens -- the same for n single tokens, each with its own
+ * radius instead of a mask buffer.
+ *   q        device bf16 [heads][n][d], 16-byte aligned
+ *   token    device int32 [n], the natural index (t*H + h)*W + w of each token
+ *            (any order, repeats allowed).  A negative index marks an unused
+ *            place: its rows of out and lse are left as they were.  An index of
+ *            N or more is recorded as TRA_ERR_DEVICE_CHECK and treated likewise.
+ *   radius   device int32 [heads][n], 0 or more; a negative radius keeps no key
+ *   out      device [heads][n][d], fp32 (bf16 with TRA_FLAG_OUT_BF16)
+ *   lse      device fp32 [heads][n]; zeros and -infinity where no cached key
+ *            is kept
+ * n = 0 does nothing.  All arithmetic is fp32.  Asynchronous on `stream`.
+ */
+TRA_API tra_status tra_cache_attention_tokens(tra_plan plan, const void* q, const int32_t* token,
+                         const int32_t* radius, int n, const void* cache, size_t cache_bytes,
+                         int cached_frames, void* out, float* lse, tra_stream stream);
+
 /*
  * tra_calibrate_topk -- calibration workload (the summary's Intuition I: the
  * key density a query needs follows its entropy, B ~ tau * exp(H_i)).  For the

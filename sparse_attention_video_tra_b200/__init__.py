@@ -18,10 +18,11 @@ import os
 from dataclasses import dataclass
 
 __all__ = [
-    "TraError", "PlanInfo", "Plan", "library_path", "load_library",
+    "TraError", "PlanInfo", "CacheInfo", "Plan", "library_path", "load_library",
     "tra_plan_create", "tra_plan_destroy", "tra_plan_query", "tra_permute", "tra_entropy",
     "tra_radius_and_mask", "tra_attention", "tra_attention_lse", "tra_attention_backward",
-    "tra_attention_backward_bytes", "tra_calibrate_topk", "tra_calibrate_fit", "tra_plan_status",
+    "tra_attention_backward_bytes", "tra_cache_query", "tra_cache_store", "tra_cache_attention",
+    "tra_cache_attention_bytes", "tra_cache_attention_tokens", "tra_calibrate_topk", "tra_calibrate_fit", "tra_plan_status",
     "tra_status_string",
     "TRA_FLAG_DEBUG_NO_WAIT", "TRA_FLAG_OUT_BF16", "TRA_FLAG_NATURAL", "TRA_FLAG_DISK", "TRA_FLAG_QSORT",
     "tra_flag_tile_w",
@@ -84,6 +85,19 @@ class PlanInfo:
     off_group: int
 
 
+class _CacheInfo(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in ("cache_bytes", "off_k", "off_v", "off_k_scale", "off_v_scale")]
+
+
+@dataclass(frozen=True)
+class CacheInfo:
+    cache_bytes: int
+    off_k: int
+    off_v: int
+    off_k_scale: int
+    off_v_scale: int
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -119,6 +133,17 @@ def load_library() -> ctypes.CDLL:
     L.tra_attention_backward.restype = st
     L.tra_attention_backward_bytes.argtypes = [vp, ctypes.POINTER(ctypes.c_size_t)]
     L.tra_attention_backward_bytes.restype = st
+    sz = ctypes.c_size_t
+    L.tra_cache_query.argtypes = [vp, ctypes.POINTER(_CacheInfo)]
+    L.tra_cache_query.restype = st
+    L.tra_cache_store.argtypes = [vp, vp, vp, i, i, vp, sz, vp]
+    L.tra_cache_store.restype = st
+    L.tra_cache_attention.argtypes = [vp, vp, i, i, vp, sz, i, vp, vp, vp, vp, sz, vp]
+    L.tra_cache_attention.restype = st
+    L.tra_cache_attention_bytes.argtypes = [vp, i, ctypes.POINTER(sz)]
+    L.tra_cache_attention_bytes.restype = st
+    L.tra_cache_attention_tokens.argtypes = [vp, vp, vp, vp, i, vp, sz, i, vp, vp, vp]
+    L.tra_cache_attention_tokens.restype = st
     L.tra_calibrate_topk.argtypes = [vp, vp, vp, ctypes.c_double, i, vp, vp, vp]
     L.tra_calibrate_topk.restype = st
     L.tra_calibrate_fit.argtypes = [vp, vp, ctypes.c_longlong, ctypes.POINTER(ctypes.c_double),
@@ -194,6 +219,37 @@ def tra_attention_backward_bytes(plan) -> int:
     n = ctypes.c_size_t()
     _check("tra_attention_backward_bytes", load_library().tra_attention_backward_bytes(plan, ctypes.byref(n)))
     return n.value
+
+
+def tra_cache_query(plan) -> CacheInfo:
+    info = _CacheInfo()
+    _check("tra_cache_query", load_library().tra_cache_query(plan, ctypes.byref(info)))
+    return CacheInfo(**{f: getattr(info, f) for f, _ in _CacheInfo._fields_})
+
+
+def tra_cache_store(plan, k_ptr, v_ptr, frame, n_frames, cache_ptr, cache_bytes, stream=0) -> None:
+    _check("tra_cache_store", load_library().tra_cache_store(plan, k_ptr, v_ptr, int(frame), int(n_frames), cache_ptr,
+                                                             int(cache_bytes), stream))
+
+
+def tra_cache_attention(plan, q_ptr, frame, n_frames, cache_ptr, cache_bytes, cached_frames, mask_ptr, out_ptr, lse_ptr,
+                        workspace_ptr, workspace_bytes, stream=0) -> None:
+    _check("tra_cache_attention", load_library().tra_cache_attention(
+        plan, q_ptr, int(frame), int(n_frames), cache_ptr, int(cache_bytes), int(cached_frames), mask_ptr, out_ptr,
+        lse_ptr, workspace_ptr, int(workspace_bytes), stream))
+
+
+def tra_cache_attention_bytes(plan, n_frames) -> int:
+    n = ctypes.c_size_t()
+    _check("tra_cache_attention_bytes", load_library().tra_cache_attention_bytes(plan, int(n_frames), ctypes.byref(n)))
+    return n.value
+
+
+def tra_cache_attention_tokens(plan, q_ptr, token_ptr, radius_ptr, n, cache_ptr, cache_bytes, cached_frames, out_ptr,
+                               lse_ptr, stream=0) -> None:
+    _check("tra_cache_attention_tokens", load_library().tra_cache_attention_tokens(
+        plan, q_ptr, token_ptr, radius_ptr, int(n), cache_ptr, int(cache_bytes), int(cached_frames), out_ptr, lse_ptr,
+        stream))
 
 
 def tra_calibrate_topk(plan, q_ptr, k_ptr, mass, query_tile_stride, H_ptr, k_out_ptr, stream=0) -> None:
@@ -407,6 +463,82 @@ class Plan:
                                out.data_ptr(), lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                                dv.data_ptr(), workspace.data_ptr(), workspace.numel(), self._stream(stream))
         return dq, dk, dv
+
+    # -- keys and values held in 8 bits
+    def new_cache(self, device="cuda"):
+        """The 8-bit cache of this plan's grid and heads, nothing stored yet."""
+        import torch
+        return torch.empty(tra_cache_query(self.handle).cache_bytes, dtype=torch.uint8, device=device)
+
+    def new_cache_workspace(self, n_frames, device="cuda"):
+        """Workspace of cache_attention for up to n_frames query frames."""
+        import torch
+        return torch.empty(tra_cache_attention_bytes(self.handle, n_frames), dtype=torch.uint8, device=device)
+
+    def cache_views(self, cache):
+        """(k codes, v codes [heads, n_tiles, 128, d] float8_e4m3fn, k scale, v scale [heads, n_tiles] fp32)."""
+        import torch
+        i, c = self.info, tra_cache_query(self.handle)
+
+        def codes(off):
+            return cache[off:off + i.heads * i.N_pad * i.d].view(torch.float8_e4m3fn).view(i.heads, i.n_tiles, 128, i.d)
+
+        def scale(off):
+            return cache[off:off + i.heads * i.n_tiles * 4].view(torch.float32).view(i.heads, i.n_tiles)
+
+        return codes(c.off_k), codes(c.off_v), scale(c.off_k_scale), scale(c.off_v_scale)
+
+    def _frames(self, x, name) -> int:
+        """How many frames of this plan's rows [heads, rows, d] x holds."""
+        i = self.info
+        per = i.H * i.W if self.natural else i.n_tiles_h * i.n_tiles_w * 128
+        if x.dim() != 3 or x.shape[0] != i.heads or x.shape[2] != i.d or x.shape[1] % per or not x.shape[1]:
+            raise ValueError(f"{name}: expected [{i.heads}, frames * {per}, {i.d}], got {tuple(x.shape)}")
+        return x.shape[1] // per
+
+    def cache_store(self, k, v, frame, cache, stream=None):
+        """tra_cache_store: k and v hold the rows of the frames from `frame` on, as many as their shape says."""
+        import torch
+        n = self._frames(k, "k")
+        for x, nme in ((k, "k"), (v, "v")):
+            self._rows(x, k.shape[1], nme)
+        self._buffer(cache, torch.uint8, 1, "cache")
+        self._on_device(k, v, cache)
+        tra_cache_store(self.handle, k.data_ptr(), v.data_ptr(), frame, n, cache.data_ptr(), cache.numel(),
+                        self._stream(stream))
+        return cache
+
+    def cache_attention(self, q, frame, cache, cached_frames, mask, out, lse, workspace, stream=None):
+        """tra_cache_attention: the queries of the frames from `frame` on, as many as q's shape says."""
+        import torch
+        i = self.info
+        n = self._frames(q, "q")
+        self._rows(q, q.shape[1], "q")
+        self._rows(out, q.shape[1], "out", self.out_dtype)
+        self._buffer(lse, torch.float32, i.heads * q.shape[1], "lse")
+        self._buffer(mask, torch.uint8, i.mask_bytes, "mask")
+        self._buffer(cache, torch.uint8, 1, "cache")
+        self._buffer(workspace, torch.uint8, 1, "workspace")
+        self._on_device(q, cache, mask, out, lse, workspace)
+        tra_cache_attention(self.handle, q.data_ptr(), frame, n, cache.data_ptr(), cache.numel(), cached_frames,
+                            mask.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                            self._stream(stream))
+        return out, lse
+
+    def cache_attention_tokens(self, q, token, radius, cache, cached_frames, out, lse, stream=None):
+        """tra_cache_attention_tokens: q [heads, n, d], token int32 [n], radius int32 [heads, n]."""
+        import torch
+        i, n = self.info, token.numel()
+        self._rows(q, n, "q")
+        self._rows(out, n, "out", self.out_dtype)
+        self._buffer(token, torch.int32, n, "token")
+        self._buffer(radius, torch.int32, i.heads * n, "radius")
+        self._buffer(lse, torch.float32, i.heads * n, "lse")
+        self._buffer(cache, torch.uint8, 1, "cache")
+        self._on_device(q, token, radius, cache, out, lse)
+        tra_cache_attention_tokens(self.handle, q.data_ptr(), token.data_ptr(), radius.data_ptr(), n, cache.data_ptr(),
+                                   cache.numel(), cached_frames, out.data_ptr(), lse.data_ptr(), self._stream(stream))
+        return out, lse
 
     def calibrate_topk(self, q, k, mass, query_tile_stride=1, stream=None):
         """Calibration workload: (H [heads, n_sample, 128] fp32, k [heads,

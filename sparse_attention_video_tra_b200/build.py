@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libtra_b200.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
-SOURCES = ["tra_api.cu", "tra_grad.cu", "tra_plan.cpp"]
+SOURCES = ["tra_api.cu", "tra_grad.cu", "tra_cache.cu", "tra_plan.cpp"]
 
 
 def _inputs():

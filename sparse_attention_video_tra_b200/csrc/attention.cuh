@@ -105,13 +105,23 @@ __device__ __forceinline__ uint32_t pack_tile(int t, int tr, int tc)
 }
 constexpr uint32_t MT_IN0 = 1u << 26, MT_FULL0 = 1u << 28;
 
+// The query and key frames of a call that reads a cache (SPAN): q, out and lse
+// hold the rows of the frames [q0, q0 + nq) only, k and v the tile-major rows
+// of the key frames [k0, k1) only.
+struct Span {
+    int q0, nq, k0, k1;
+};
+
 // LSE: also write each row's log-sum-exp (natural log) to `lse`; O is then
 // normalised by the sum of the unrounded P, which is the sum the log is of.
-template <int D, int TWL, bool OUT_BF16, bool DISK, bool LSE>
+// SPAN (with LSE): the queries of some frames over the keys of some frames;
+// listed key tiles outside them are passed over, and a row that is left with
+// no key gets zeros and -inf.
+template <int D, int TWL, bool OUT_BF16, bool DISK, bool LSE, bool SPAN>
 __global__ void __launch_bounds__(384, 1)
 attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const Geom G, const uint8_t* __restrict__ mask,
-                 void* __restrict__ out, const void* __restrict__ qraw, float* __restrict__ lse)
+                 void* __restrict__ out, const void* __restrict__ qraw, float* __restrict__ lse, const Span span)
 {
     using C = AttnCfg<D>;
     constexpr int TW = 1 << TWL;
@@ -150,16 +160,42 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // (slots 2k and 2k + 1 of that frame, neighbouring strips), so that no
     // CTA runs a lone chain while a slot of the frame is left to pair with.
     const int tpf = G.tiles_per_frame;
-    const int paired = (G.T / 2) * tpf;                 // CTAs of the frame pairs
-    int qa = 2 * pair, qb = qa + 1;
+    const int q0 = SPAN ? span.q0 : 0, nq = SPAN ? span.nq : G.T;   // the call's query frames
+    const int paired = (nq / 2) * tpf;                  // CTAs of the frame pairs
+    int qa = q0 * tpf + 2 * pair, qb = qa + 1;
     if (G.qsort && pair < paired) {
-        qa = 2 * (pair / tpf) * tpf + pair % tpf;
+        qa = (q0 + 2 * (pair / tpf)) * tpf + pair % tpf;
         qb = qa + tpf;
     } else if (G.qsort) {
-        qa = (G.T - 1) * tpf + 2 * (pair - paired);
+        qa = (q0 + nq - 1) * tpf + 2 * (pair - paired);
         qb = qa + 1;
     }
-    const bool hasB = qb < G.nQ;
+    const bool hasB = qb < (q0 + nq) * tpf;
+    // the row of token (t, h, w) in q, out and lse
+    auto query_row = [&](int t, int h, int w, int tile_row) -> size_t {
+        if constexpr (SPAN)
+            return G.natural ? (size_t)g * nq * (G.H * G.W) + ((size_t)(t - q0) * G.H + h) * G.W + w
+                             : (size_t)g * nq * (tpf * 128) + (tile_row - q0 * tpf * 128);
+        else
+            return io_row(G, g, t, h, w, tile_row);
+    };
+    // one panel of a query tile, and of a key tile, into shared memory
+    auto load_query_panel = [&](void* dst, int p, int t, int tr, int tc, uint64_t* bar) {
+        if constexpr (SPAN) {
+            if (G.natural)
+                tma_load_4d(dst, &tm_q, p * 64, tc * G.tw, tr * G.th, g * nq + t - q0, bar);
+            else
+                tma_load_2d(dst, &tm_q, p * 64, (g * nq * tpf + ((t - q0) * G.nTh + tr) * G.nTw + tc) * 128, bar);
+        } else {
+            load_tile_panel(dst, &tm_q, G, p, g, t, tr, tc, bar);
+        }
+    };
+    auto load_key_panel = [&](void* dst, const CUtensorMap* m, int p, int t, int tr, int tc, uint64_t* bar) {
+        if constexpr (SPAN)
+            tma_load_2d(dst, m, p * 64, (g * (span.k1 - span.k0) * tpf + ((t - span.k0) * G.nTh + tr) * G.nTw + tc) * 128, bar);
+        else
+            load_tile_panel(dst, m, G, p, g, t, tr, tc, bar);
+    };
     const int32_t* counts = reinterpret_cast<const int32_t*>(mask + G.off_count) + (size_t)g * G.nQ;
     const uint16_t* lists = reinterpret_cast<const uint16_t*>(mask + G.off_list) + (size_t)g * G.nQ * G.list_cap;
     int nA = counts[qa], nB = hasB ? counts[qb] : 0;
@@ -188,6 +224,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             atomicOr(&g_tra_error, TRA_ERRBIT_CHECK);
             continue;
         }
+        if (SPAN && (fe < span.k0 || fe >= span.k1)) continue;     // not among the call's key frames
         atomicOr(&bits[(isB ? 1 : 0) * L.bw + (bit >> 5)], 1u << (bit & 31));
         if (e & 0x8000) atomicOr(&bits[(isB ? 3 : 2) * L.bw + (bit >> 5)], 1u << (bit & 31));
     }
@@ -310,8 +347,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_arrive_expect_tx(&(isK ? k_full : v_full)[j], C::TILE);
 #pragma unroll
             for (int p = 0; p < C::NP; ++p)
-                load_tile_panel((isK ? sK : sV) + j * C::TILE + p * C::PANEL, isK ? &tm_k : &tm_v, G, p, g, tk, trk, tck,
-                                &(isK ? k_full : v_full)[j]);
+                load_key_panel((isK ? sK : sV) + j * C::TILE + p * C::PANEL, isK ? &tm_k : &tm_v, p, tk, trk, tck,
+                               &(isK ? k_full : v_full)[j]);
         }
     }
     // radius-sorted query groups: row r of slot s holds strip row grp_s[r] of
@@ -342,7 +379,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     const int hq = (l >> 7) * G.th + ((l & 127) >> TWL), wq = tcq * TW + (l & (TW - 1));
                     if (hq < G.H && wq < G.W) {
                         const int tl = (tq * G.nTh + (l >> 7)) * G.nTw + tcq;
-                        const size_t qrow = io_row(G, g, tq, hq, wq, tl * 128 + (l & 127));
+                        const size_t qrow = query_row(tq, hq, wq, tl * 128 + (l & 127));
                         qv[k] = __ldg(reinterpret_cast<const uint4*>(qraw) + qrow * CH + ch);
                     }
                 }
@@ -380,8 +417,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 tile_coords(G, hasB ? qb : qa, tqb, trqb, tcqb);
 #pragma unroll
                 for (int p = 0; p < C::NP; ++p) {
-                    load_tile_panel(sQ + p * C::PANEL, &tm_q, G, p, g, tqa, trqa, tcqa, q_full);
-                    if (hasB) load_tile_panel(sQ + C::TILE + p * C::PANEL, &tm_q, G, p, g, tqb, trqb, tcqb, q_full);
+                    load_query_panel(sQ + p * C::PANEL, p, tqa, trqa, tcqa, q_full);
+                    if (hasB) load_query_panel(sQ + C::TILE + p * C::PANEL, p, tqb, trqb, tcqb, q_full);
                 }
             }
             static_assert(C::KST == C::VST, "one ring depth for K and V");
@@ -399,7 +436,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 mbar_arrive_expect_tx(&fullb[st], C::TILE);
 #pragma unroll
                 for (int p = 0; p < C::NP; ++p)
-                    load_tile_panel(ring + st * C::TILE + p * C::PANEL, tm, G, p, g, tk, trk, tck, &fullb[st]);
+                    load_key_panel(ring + st * C::TILE + p * C::PANEL, tm, p, tk, trk, tck, &fullb[st]);
                 ++iss;
             }
             // copies still in flight must land before the CTA exits
@@ -686,22 +723,27 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_arrive(&p_full[w]);
             ++k;
         }
-        if (ok && k > 0) {
-            ok = role_wait(&pv_done[w], (k - 1) & 1, G.wait_ns, s_abort);
+        if (ok && (k > 0 || (SPAN && active))) {
+            ok = k == 0 || role_wait(&pv_done[w], (k - 1) & 1, G.wait_ns, s_abort);
             if (__all_sync(0xffffffffu, ok)) {
                 tc_fence_after();
                 __syncwarp();
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 const bool store = !G.natural || qvalid;          // natural layout has no pad rows
-                const size_t orow = io_row(G, g, tq, hq, wq, qt * 128 + qrow) * D;
+                const size_t orow = query_row(tq, hq, wq, qt * 128 + qrow) * D;
                 if constexpr (LSE) {
                     if (store) lse[orow / D] = l > 0.f ? (m_run + log2f(l)) * 0.69314718055994531f : -INFINITY;
                 }
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t v[32];
-                    tmem_ld32(tmem + lane_base + colO + c * 32, v);
-                    tmem_wait_ld();
+                    if (SPAN && k == 0) {                          // no key of the call: O was never written
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0u;
+                    } else {
+                        tmem_ld32(tmem + lane_base + colO + c * 32, v);
+                        tmem_wait_ld();
+                    }
                     if (!store) continue;
                     if constexpr (OUT_BF16) {
                         uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + orow + c * 32);

@@ -7,50 +7,51 @@
 
 namespace {
 
-template <int D, int TWL, bool OB, bool DISK, bool LSE>
+template <int D, int TWL, bool OB, bool DISK, bool LSE, bool SPAN>
 tra_status run_attention(const tra::Geom& G, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                          const uint8_t* mask, void* out, const void* qraw, float* lse,
-                         cudaStream_t st)
+                         const tra::Span& span, cudaStream_t st)
 {
     using C = tra::AttnCfg<D>;
-    auto kern = tra::attention_kernel<D, TWL, OB, DISK, LSE>;
+    auto kern = tra::attention_kernel<D, TWL, OB, DISK, LSE, SPAN>;
     const int smem = tra::attn_smem_bytes<D>(G.list_cap, G.rte, G.tiles_per_frame);
     if (smem > kMaxSmem) return TRA_ERR_UNSUPPORTED;
     if (!set_smem(kern, smem)) return TRA_ERR_CUDA;
     // two query tiles per CTA; with radius-sorted groups, the same slot of
     // frames 2f and 2f + 1, then an odd last frame's slots two by two
-    const int ctas = G.qsort ? G.T / 2 * G.tiles_per_frame + (G.T % 2) * ((G.tiles_per_frame + 1) / 2)
-                             : (G.nQ + 1) / 2;
-    kern<<<dim3(ctas, G.G), C::THREADS, smem, st>>>(q, k, v, G, mask, out, qraw, lse);
+    const int nq = SPAN ? span.nq : G.T;
+    const int ctas = G.qsort ? nq / 2 * G.tiles_per_frame + (nq % 2) * ((G.tiles_per_frame + 1) / 2)
+                             : (nq * G.tiles_per_frame + 1) / 2;
+    kern<<<dim3(ctas, G.G), C::THREADS, smem, st>>>(q, k, v, G, mask, out, qraw, lse, span);
     return launch_status();
 }
 
-template <int D, int TWL, bool LSE>
+template <int D, int TWL, bool LSE, bool SPAN>
 tra_status attention_variant(const tra::Geom& G, bool ob, bool disk, const CUtensorMap& q, const CUtensorMap& k,
                              const CUtensorMap& v, const uint8_t* m, void* out, const void* qr, float* lse,
-                             cudaStream_t st)
+                             const tra::Span& span, cudaStream_t st)
 {
-    if (ob) return disk ? run_attention<D, TWL, true, true, LSE>(G, q, k, v, m, out, qr, lse, st)
-                        : run_attention<D, TWL, true, false, LSE>(G, q, k, v, m, out, qr, lse, st);
-    return disk ? run_attention<D, TWL, false, true, LSE>(G, q, k, v, m, out, qr, lse, st)
-                : run_attention<D, TWL, false, false, LSE>(G, q, k, v, m, out, qr, lse, st);
+    if (ob) return disk ? run_attention<D, TWL, true, true, LSE, SPAN>(G, q, k, v, m, out, qr, lse, span, st)
+                        : run_attention<D, TWL, true, false, LSE, SPAN>(G, q, k, v, m, out, qr, lse, span, st);
+    return disk ? run_attention<D, TWL, false, true, LSE, SPAN>(G, q, k, v, m, out, qr, lse, span, st)
+                : run_attention<D, TWL, false, false, LSE, SPAN>(G, q, k, v, m, out, qr, lse, span, st);
 }
 
 // kernel instance by (head dim, tile width, output type, spatial metric)
-template <bool LSE>
+template <bool LSE, bool SPAN>
 tra_status dispatch_attention(const tra::Geom& G, bool ob, bool disk, const CUtensorMap& q, const CUtensorMap& k,
                               const CUtensorMap& v, const uint8_t* m, void* out, const void* qr, float* lse,
-                             cudaStream_t st)
+                             const tra::Span& span, cudaStream_t st)
 {
     switch (G.D * 100 + G.tw_log2) {
-        case 6402: return attention_variant<64, 2, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
-        case 6403: return attention_variant<64, 3, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
-        case 6404: return attention_variant<64, 4, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
-        case 6405: return attention_variant<64, 5, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
-        case 12802: return attention_variant<128, 2, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
-        case 12803: return attention_variant<128, 3, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
-        case 12804: return attention_variant<128, 4, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
-        case 12805: return attention_variant<128, 5, LSE>(G, ob, disk, q, k, v, m, out, qr, lse, st);
+        case 6402: return attention_variant<64, 2, LSE, SPAN>(G, ob, disk, q, k, v, m, out, qr, lse, span, st);
+        case 6403: return attention_variant<64, 3, LSE, SPAN>(G, ob, disk, q, k, v, m, out, qr, lse, span, st);
+        case 6404: return attention_variant<64, 4, LSE, SPAN>(G, ob, disk, q, k, v, m, out, qr, lse, span, st);
+        case 6405: return attention_variant<64, 5, LSE, SPAN>(G, ob, disk, q, k, v, m, out, qr, lse, span, st);
+        case 12802: return attention_variant<128, 2, LSE, SPAN>(G, ob, disk, q, k, v, m, out, qr, lse, span, st);
+        case 12803: return attention_variant<128, 3, LSE, SPAN>(G, ob, disk, q, k, v, m, out, qr, lse, span, st);
+        case 12804: return attention_variant<128, 4, LSE, SPAN>(G, ob, disk, q, k, v, m, out, qr, lse, span, st);
+        case 12805: return attention_variant<128, 5, LSE, SPAN>(G, ob, disk, q, k, v, m, out, qr, lse, span, st);
     }
     return TRA_ERR_UNSUPPORTED;
 }

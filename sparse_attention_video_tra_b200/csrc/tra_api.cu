@@ -127,7 +127,7 @@ extern "C" tra_status tra_attention(tra_plan plan, const void* q, const void* k,
     const uint8_t* m = (const uint8_t*)mask;
     const bool ob = (plan->flags & TRA_FLAG_OUT_BF16) != 0;
     const bool disk = G.disk != 0;
-    return dispatch_attention<false>(G, ob, disk, mq, mk, mv, m, out, q, nullptr, st);
+    return dispatch_attention<false, false>(G, ob, disk, mq, mk, mv, m, out, q, nullptr, {}, st);
 }
 
 extern "C" tra_status tra_calibrate_topk(tra_plan plan, const void* q, const void* k, double mass,
@@ -159,7 +159,7 @@ extern "C" tra_status tra_plan_status(tra_plan plan)
 {
     (void)plan;
     unsigned int word = 0;
-    if (!take_error_word(word) || !tra_grad_take_error(word)) return TRA_ERR_CUDA;
+    if (!take_error_word(word) || !tra_grad_take_error(word) || !tra_cache_take_error(word)) return TRA_ERR_CUDA;
     if (word & TRA_ERRBIT_TIMEOUT) return TRA_ERR_TIMEOUT;
     if (word & TRA_ERRBIT_CHECK) return TRA_ERR_DEVICE_CHECK;
     return TRA_OK;

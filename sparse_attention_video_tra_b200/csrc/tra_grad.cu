@@ -16,8 +16,8 @@ extern "C" tra_status tra_attention_lse(tra_plan plan, const void* q, const void
     CUtensorMap mq, mk, mv;
     if (!make_input_map(&mq, q, G) || !make_input_map(&mk, k, G) || !make_input_map(&mv, v, G))
         return TRA_ERR_CUDA;
-    return dispatch_attention<true>(G, (plan->flags & TRA_FLAG_OUT_BF16) != 0, G.disk != 0, mq, mk, mv,
-                                    (const uint8_t*)mask, out, q, lse, (cudaStream_t)stream);
+    return dispatch_attention<true, false>(G, (plan->flags & TRA_FLAG_OUT_BF16) != 0, G.disk != 0, mq, mk, mv,
+                                    (const uint8_t*)mask, out, q, lse, {}, (cudaStream_t)stream);
 }
 
 namespace {

@@ -14,3 +14,4 @@ struct tra_plan_s {
 
 // read and clear the error word of the other translation units' kernels
 bool tra_grad_take_error(unsigned int& word);
+bool tra_cache_take_error(unsigned int& word);

@@ -14,9 +14,9 @@ BF16 = 2.0 ** -8
 FP32 = 2.0 ** -24
 
 
-def token_mask(T, H, W, gamma, Rt, radius, disk=False, first=0, cached=None):
-    """[heads, n, m]: query `first + i` of radius[:, i] keeps key j of the first `cached` frames (all T by default)."""
-    n = torch.arange(first, first + radius.shape[1], device=radius.device)
+def token_mask(T, H, W, gamma, Rt, radius, disk=False, frame=0, cached=None):
+    """[heads, n, m]: query i (radius[:, i]) of the frames from `frame` on keeps key j of the first `cached` frames (all T by default)."""
+    n = frame * H * W + torch.arange(radius.shape[1], device=radius.device)
     m = torch.arange((T if cached is None else cached) * H * W, device=radius.device)
     return pairs_kept(T, H, W, gamma, Rt, n, m, radius, disk)
 
@@ -34,8 +34,9 @@ def pairs_kept(T, H, W, gamma, Rt, n, m, radius, disk=False):
     return keep
 
 
-def attention(q, k, v, keep):
-    """(out, lse, bound of out before its own rounding, bound of lse); rows that keep nothing: 0 and -inf."""
+def attention(q, k, v, keep, p_round=BF16):
+    """(out, lse, bound of out before its own rounding, bound of lse); rows that keep nothing: 0 and -inf.
+    p_round: what the probabilities are rounded by before the product with v (0: not rounded)."""
     q, k, v = q.double(), k.double(), v.double()
     d = q.shape[-1]
     x = (q @ k.mT / math.sqrt(d)).masked_fill(~keep, -math.inf)
@@ -46,8 +47,9 @@ def attention(q, k, v, keep):
     dx = (q.abs() @ k.abs().mT / math.sqrt(d)) * ((d + 4) * FP32) + 2.0 ** -20 * (1 + x.masked_fill(~keep, 0.0).abs())
     # numerator and denominator each carry P's error; P is also rounded to bf16 (the numerator alone)
     err = (p * dx).sum(-1)
-    out_err = (p * (BF16 + dx)) @ v.abs() + (err + 2.0 ** -16)[..., None] * (p @ v.abs())
+    out_err = (p * (p_round + dx)) @ v.abs() + (err + 2.0 ** -16)[..., None] * (p @ v.abs())
     lse_err = err + 2.0 ** -18 * (1 + lse.nan_to_num(neginf=0.0).abs())
+    # a row of no keys has no error to allow
     return out, lse, out_err, lse_err
 
 
@@ -73,6 +75,9 @@ def gradients(q, k, v, out, lse, dout, keep):
 def check(got, ref, bound, name=""):
     """got within bound plus got's own rounding of ref."""
     got64 = got.double()
+    nothing = ref == -math.inf
+    assert torch.equal(got64 == -math.inf, nothing), name
+    got64, ref, bound = (x.masked_fill(nothing, 0.0) for x in (got64, ref, bound))
     step = BF16 if got.dtype == torch.bfloat16 else FP32
     tol = bound * (1 + step) + ref.abs() * step + 1e-30
     over = (got64 - ref).abs() - tol
