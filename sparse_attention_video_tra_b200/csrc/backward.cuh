@@ -219,12 +219,13 @@ __device__ __forceinline__ void store_cols32(void* base, bool bf16, size_t elem,
 //              fp32 and written back over S^T as bf16), then reads dP^T and
 //              writes dS^T over it.
 //   warp 8     TMA: K, V once, then the rings of Q and dO.
-//   warp 9     MMA issuer.  Per slot j, two groups alternate with the two
-//              halves of the elementwise work: {dV += P^T dO, S^T of slot j+1}
-//              while dS^T of j is made, {dK += dS^T Q, dP^T of slot j+1} while
-//              P^T of j+1 is made.  MMAs of one thread run in order, so S^T of
-//              j+1 overwrites P^T of j only after dV has read it, and dP^T of
-//              j+1 overwrites dS^T of j only after dK has.
+//   warp 9     MMA issuer.  Each half of a slot is a chain of its own:
+//              {dV += P^T dO, S^T of slot j+1} once P^T of slot j is there, and
+//              {dK += dS^T Q, dP^T of slot j+1} once dS^T is; the groups of the
+//              two halves alternate, so one half's elementwise work runs
+//              under the other's products.  MMAs of one thread run in order,
+//              so S^T of j+1 overwrites P^T of j only after dV has read it, and
+//              dP^T of j+1 overwrites dS^T of j only after dK has.
 //   warps 10, 11  per slot, the 64 queries' lse and D_i and the keep-bits of
 //              all 128 keys into a two-stage ring (and whether all are set:
 //              such halves skip the masking).
@@ -239,7 +240,7 @@ struct BwdKvCfg {
     static constexpr int ST = 2;                            // Q and dO ring depth
     static constexpr int OFF_K = 0, OFF_V = TILE;
     static constexpr int OFF_Q = 2 * TILE, OFF_DO = OFF_Q + ST * TILE;
-    static constexpr int OFF_META = OFF_DO + ST * TILE;     // [ST][2 halves]: lse[64], D[64], words[4][64]
+    static constexpr int OFF_META = OFF_DO + ST * TILE;     // [ST][2 halves]: -lse[64], -D[64], words[4][64]
     static constexpr int META = 64 * 4 * 6;                 // bytes of a half
     static constexpr int OFF_BARS = OFF_META + ST * 2 * META;
     static constexpr int OFF_LIST = OFF_BARS + 32 * 8 + 64; // uint16 [list_cap]
@@ -266,11 +267,11 @@ backward_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint64_t* do_empty = do_full + C::ST;
     uint64_t* meta_full = do_empty + C::ST;      // [ST][2]
     uint64_t* meta_empty = meta_full + 2 * C::ST;
-    uint64_t* s_full = meta_empty + 2 * C::ST;
-    uint64_t* dp_full = s_full + 1;
-    uint64_t* p_full = dp_full + 1;
-    uint64_t* ds_full = p_full + 1;
-    uint64_t* done = ds_full + 1;
+    uint64_t* s_full = meta_empty + 2 * C::ST;   // [2], as the following: one per half
+    uint64_t* dp_full = s_full + 2;
+    uint64_t* p_full = dp_full + 2;
+    uint64_t* ds_full = p_full + 2;
+    uint64_t* done = ds_full + 2;
     int* misc = reinterpret_cast<int*>(bars + 32);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc);
     volatile int* s_abort = misc + 1;
@@ -312,8 +313,10 @@ backward_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mbar_init(&do_full[i], 1); mbar_init(&do_empty[i], 1);
         }
         for (int i = 0; i < 2 * C::ST; ++i) { mbar_init(&meta_full[i], 32); mbar_init(&meta_empty[i], 128); }
-        mbar_init(s_full, 1); mbar_init(dp_full, 1);
-        mbar_init(p_full, 256); mbar_init(ds_full, 256);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1); mbar_init(&dp_full[i], 1);
+            mbar_init(&p_full[i], 128); mbar_init(&ds_full[i], 128);
+        }
         mbar_init(done, 1);
         *s_abort = 0;
         fence_barrier_init();
@@ -328,7 +331,7 @@ backward_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (warp >= 8) {
         regs_dec<C::REGS_OTHER>();
         if (warp == 8) {
-            if (lane == 0 && n > 0) {
+            if (n > 0 && elect_one()) {
                 prefetch_tmap(&tm_q); prefetch_tmap(&tm_k); prefetch_tmap(&tm_v); prefetch_tmap(&tm_do);
                 int iss_q = 0, iss_do = 0;
                 auto load_q = [&](int j) -> bool {
@@ -366,56 +369,68 @@ backward_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 for (int j = max(0, iss_do - C::ST); j < iss_do; ++j) mbar_wait(&do_full[j % C::ST], (j / C::ST) & 1, G.drain_ns);
             }
         } else if (warp == 9) {
-            if (lane == 0 && n > 0) {
-                constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, false);
+            if (n > 0 && elect_one()) {
+                constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 64, false);
                 constexpr uint32_t IDESC_G = idesc_bf16_f32(128, D, true);
                 const uint32_t sK = smem_u32(smem + C::OFF_K), sV = smem_u32(smem + C::OFF_V);
                 const uint32_t sQ = smem_u32(smem + C::OFF_Q), sD = smem_u32(smem + C::OFF_DO);
-                // A (keys) times B^T (queries), both K-major
-                auto scores = [&](uint32_t col, uint32_t a, uint32_t b) {
+                // A (keys) times B^T (the 64 queries of half u), both K-major
+                auto scores = [&](uint32_t col, uint32_t a, uint32_t b, int u) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * C::PANEL + (kk & 3) * 32;
-                        mma_ss(tmem + col, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off, 16, 1024), IDESC_S, kk > 0 ? 1u : 0u);
+                        mma_ss(tmem + col + u * 64, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off + u * 8192, 16, 1024),
+                               IDESC_S, kk > 0 ? 1u : 0u);
                     }
                 };
-                // the bf16 pairs in the two halves of `col` times the rows of b
-                auto accumulate = [&](uint32_t dst, uint32_t col, uint32_t b, bool add) {
+                // the bf16 pairs in half u of `col` times the 64 rows of half u of b
+                auto accumulate = [&](uint32_t dst, uint32_t col, uint32_t b, int u, bool add) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_ts(tmem + dst, tmem + col + (kk >> 2) * 64 + (kk & 3) * 8,
-                               smem_desc_sw128(b + kk * 2048, C::PANEL, 1024), IDESC_G, (add || kk > 0) ? 1u : 0u);
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ts(tmem + dst, tmem + col + u * 64 + kk * 8,
+                               smem_desc_sw128(b + u * 8192 + kk * 2048, C::PANEL, 1024), IDESC_G, (add || kk > 0) ? 1u : 0u);
                 };
                 bool ok = role_wait(kv_full, 0, G.wait_ns, s_abort) && role_wait(&q_full[0], 0, G.wait_ns, s_abort);
                 if (ok) {
                     tc_fence_after();
-                    scores(COL_S, sK, sQ);
-                    mma_commit(s_full);
+                    for (int u = 0; u < 2; ++u) {
+                        scores(COL_S, sK, sQ, u);
+                        mma_commit(&s_full[u]);
+                    }
                     ok = role_wait(&do_full[0], 0, G.wait_ns, s_abort);
                 }
                 if (ok) {
-                    scores(COL_DP, sV, sD);
-                    mma_commit(dp_full);
+                    for (int u = 0; u < 2; ++u) {
+                        scores(COL_DP, sV, sD, u);
+                        mma_commit(&dp_full[u]);
+                    }
                 }
                 for (int j = 0; ok && j < n; ++j) {
                     const int st = j % C::ST, sn = (j + 1) % C::ST;
-                    if (!role_wait(p_full, j & 1, G.wait_ns, s_abort)) break;
-                    tc_fence_after();
-                    accumulate(COL_DV, COL_S, sD + st * C::TILE, j > 0);
-                    mma_commit(&do_empty[st]);
-                    if (j + 1 < n) {
-                        if (!role_wait(&q_full[sn], ((j + 1) / C::ST) & 1, G.wait_ns, s_abort)) break;
-                        scores(COL_S, sK, sQ + sn * C::TILE);
-                        mma_commit(s_full);
+                    const bool next = j + 1 < n;
+                    for (int u = 0; ok && u < 2; ++u) {
+                        ok = role_wait(&p_full[u], j & 1, G.wait_ns, s_abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        accumulate(COL_DV, COL_S, sD + st * C::TILE, u, j > 0 || u > 0);
+                        if (u == 1) mma_commit(&do_empty[st]);
+                        if (!next) continue;
+                        if (u == 0) ok = role_wait(&q_full[sn], ((j + 1) / C::ST) & 1, G.wait_ns, s_abort);
+                        if (!ok) break;
+                        scores(COL_S, sK, sQ + sn * C::TILE, u);
+                        mma_commit(&s_full[u]);
                     }
-                    if (!role_wait(ds_full, j & 1, G.wait_ns, s_abort)) break;
-                    tc_fence_after();
-                    accumulate(COL_DK, COL_DP, sQ + st * C::TILE, j > 0);
-                    mma_commit(&q_empty[st]);
-                    if (j + 1 < n) {
-                        if (!role_wait(&do_full[sn], ((j + 1) / C::ST) & 1, G.wait_ns, s_abort)) break;
-                        scores(COL_DP, sV, sD + sn * C::TILE);
-                        mma_commit(dp_full);
+                    for (int u = 0; ok && u < 2; ++u) {
+                        ok = role_wait(&ds_full[u], j & 1, G.wait_ns, s_abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        accumulate(COL_DK, COL_DP, sQ + st * C::TILE, u, j > 0 || u > 0);
+                        if (u == 1) mma_commit(&q_empty[st]);
+                        if (!next) continue;
+                        if (u == 0) ok = role_wait(&do_full[sn], ((j + 1) / C::ST) & 1, G.wait_ns, s_abort);
+                        if (!ok) break;
+                        scores(COL_DP, sV, sD + sn * C::TILE, u);
+                        mma_commit(&dp_full[u]);
                     }
                 }
                 // every issued MMA must finish before the results are read and TMEM is freed
@@ -446,8 +461,8 @@ backward_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (__any_sync(0xffffffffu, !got)) break;
                 float* f = reinterpret_cast<float*>(smem + C::OFF_META + ring * C::META);
                 uint32_t* wd = reinterpret_cast<uint32_t*>(f + 128);
-                f[lane] = r0.x; f[lane + 32] = r1.x;
-                f[64 + lane] = r0.y; f[96 + lane] = r1.y;
+                f[lane] = -r0.x; f[lane + 32] = -r1.x;
+                f[64 + lane] = -r0.y; f[96 + lane] = -r1.y;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     wd[k * 64 + lane] = m[0][k];
@@ -470,27 +485,28 @@ backward_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         for (int j = 0; j < n; ++j) {
             const int ring = (j % C::ST) * 2 + u;
             bool got = role_wait(&meta_full[ring], (j / C::ST) & 1, G.wait_ns, s_abort);
-            got = got && role_wait(s_full, j & 1, G.wait_ns, s_abort);
+            got = got && role_wait(&s_full[u], j & 1, G.wait_ns, s_abort);
             if (__any_sync(0xffffffffu, !got)) { ok = false; break; }
             tc_fence_after();
             __syncwarp();
-            const float4* lse4 = reinterpret_cast<const float4*>(smem + C::OFF_META + ring * C::META);
-            const float4* dd4 = lse4 + 16;
-            const uint4* wd4 = reinterpret_cast<const uint4*>(lse4 + 32) + (warp & 3) * 16;
+            const ulonglong2* lse2 = reinterpret_cast<const ulonglong2*>(smem + C::OFF_META + ring * C::META);
+            const ulonglong2* dd2 = lse2 + 16;
+            const uint4* wd4 = reinterpret_cast<const uint4*>(lse2 + 32) + (warp & 3) * 16;
             const bool all = s_all[ring] != 0;
+            uint32_t v[2][32];
+            tmem_ld32(colS, v[0]);
+            tmem_ld32(colS + 32, v[1]);
+            tmem_wait_ld();
             f2_t p[32];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                uint32_t v[32];
-                tmem_ld32(colS + c * 32, v);
-                tmem_wait_ld();
                 uint32_t pk[16];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float4 l = lse4[c * 8 + i];
+                    const ulonglong2 l = lse2[c * 8 + i];
                     float x0, x1, x2, x3;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), sc2, f2_pack(-l.x, -l.y)), x0, x1);
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), sc2, f2_pack(-l.z, -l.w)), x2, x3);
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c][4 * i]), __uint_as_float(v[c][4 * i + 1])), sc2, l.x), x0, x1);
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c][4 * i + 2]), __uint_as_float(v[c][4 * i + 3])), sc2, l.y), x2, x3);
                     if (!all) {
                         const uint4 m = wd4[c * 8 + i];
                         x0 = (m.x & lbit) ? x0 : -INFINITY;
@@ -508,23 +524,23 @@ backward_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(p_full);
-            got = role_wait(dp_full, j & 1, G.wait_ns, s_abort);
+            mbar_arrive(&p_full[u]);
+            got = role_wait(&dp_full[u], j & 1, G.wait_ns, s_abort);
             if (__any_sync(0xffffffffu, !got)) { ok = false; break; }
             tc_fence_after();
             __syncwarp();
+            tmem_ld32(colP, v[0]);
+            tmem_ld32(colP + 32, v[1]);
+            tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                uint32_t v[32];
-                tmem_ld32(colP + c * 32, v);
-                tmem_wait_ld();
                 uint32_t pk[16];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float4 dd = dd4[c * 8 + i];
+                    const ulonglong2 dd = dd2[c * 8 + i];
                     float x0, x1, x2, x3;
-                    f2_unpack(f2_mul(p[c * 16 + 2 * i], f2_add(f2_pack(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), f2_pack(-dd.x, -dd.y))), x0, x1);
-                    f2_unpack(f2_mul(p[c * 16 + 2 * i + 1], f2_add(f2_pack(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), f2_pack(-dd.z, -dd.w))), x2, x3);
+                    f2_unpack(f2_mul(p[c * 16 + 2 * i], f2_add(f2_pack(__uint_as_float(v[c][4 * i]), __uint_as_float(v[c][4 * i + 1])), dd.x)), x0, x1);
+                    f2_unpack(f2_mul(p[c * 16 + 2 * i + 1], f2_add(f2_pack(__uint_as_float(v[c][4 * i + 2]), __uint_as_float(v[c][4 * i + 3])), dd.y)), x2, x3);
                     pk[2 * i] = pack_bf16x2(x0, x1);
                     pk[2 * i + 1] = pack_bf16x2(x2, x3);
                 }
@@ -532,7 +548,7 @@ backward_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(ds_full);
+            mbar_arrive(&ds_full[u]);
             mbar_arrive(&meta_empty[ring]);
         }
         // warpgroup 0 writes dV, warpgroup 1 dK; a key tile that no slot lists gets zeros
@@ -652,7 +668,7 @@ backward_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     if (warp >= 8) {
         regs_dec<C::REGS_OTHER>();
         if (warp == 8) {
-            if (lane == 0 && n > 0) {
+            if (n > 0 && elect_one()) {
                 prefetch_tmap(&tm_q); prefetch_tmap(&tm_k); prefetch_tmap(&tm_v); prefetch_tmap(&tm_do);
                 mbar_arrive_expect_tx(q_full, 2 * C::TILE);
 #pragma unroll
@@ -683,7 +699,7 @@ backward_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 for (int j = max(0, iss_v - C::VST); j < iss_v; ++j) mbar_wait(&v_full[j % C::VST], (j / C::VST) & 1, G.drain_ns);
             }
         } else if (warp == 9) {
-            if (lane == 0 && n > 0) {
+            if (n > 0 && elect_one()) {
                 constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, false);
                 constexpr uint32_t IDESC_G = idesc_bf16_f32(128, D, true);
                 const uint32_t sQ = smem_u32(smem + C::OFF_Q), sD = smem_u32(smem + C::OFF_DO);
