@@ -7,9 +7,8 @@
 //     dQ_i = sum_j dS_ij k_j / sqrt d.
 // Four launches after a memset of the tile bitmaps:
 //   backward_rows   D_i, the log2-domain lse and the grid position of every
-//                   query row in mask-slot order; dO (and with query groups Q)
-//                   copied to that order where the caller's rows cannot be
-//                   read by TMA as they are
+//                   query row in mask-slot order, and the operands copied to
+//                   plain rows where the caller's are not
 //   transpose_lists the mask's key-tile lists as bits per (key tile, query slot)
 //   backward_kv     one CTA per key tile: dK and dV over the query slots that
 //                   list it
@@ -23,6 +22,8 @@
 // P and dS are rounded to bf16 for the tensor cores (at most 2^-8 of each
 // value, as P in the forward pass); all sums are fp32.
 #pragma once
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "pipeline.cuh"
@@ -35,7 +36,6 @@ struct BwdArgs {
     const float4* rows;          // [heads][nQ][128] slot order: lse * log2 e, D_i, h | w << 8 (bits), radius (bits)
     const uint32_t* bits;        // [heads][nQ key tiles][bw]: bit q - first(key tile) = slot q lists the tile
     int bw;
-    int q_natural, do_natural;   // Q / dO read from the caller's natural rows (else [heads][N_pad] rows in slot order)
     int out_bf16;                // gradients in bf16 instead of fp32
     void *dq, *dk, *dv;
     float grad_scale;            // 1 / sqrt d
@@ -50,86 +50,104 @@ __host__ __device__ inline int first_reach(const Geom& G, int tile)
 
 __host__ __device__ inline int reach_words(const Geom& G) { return (G.list_cap + 31) / 32; }
 
-__device__ __forceinline__ void load_panel(void* dst, const CUtensorMap* m, bool natural, const Geom& G, int p, int g,
-                                           int tile, uint64_t* bar)
+// one 64-column panel of tile (or slot) `tile` of head g
+__device__ __forceinline__ void load_panel(void* dst, const CUtensorMap* m, const Geom& G, int p, int g, int tile, uint64_t* bar)
 {
-    if (natural) {
-        int t, tr, tc;
-        tile_coords(G, tile, t, tr, tc);
-        tma_load_4d(dst, m, p * 64, tc * G.tw, tr * G.th, g * G.T + t, bar);
-    } else {
-        tma_load_2d(dst, m, p * 64, g * G.N_pad + tile * 128, bar);
-    }
+    tma_load_2d(dst, m, p * 64, g * G.N_pad + tile * 128, bar);
 }
 
 // ------------------------------------------------------------------ row data
-// One warp per row of a mask slot.  IN_F32: dout and out are fp32 (else bf16).
-// dO is rounded to bf16 first and D_i taken from the rounded values, the ones
-// the products use.  HBM-bound.
+// What the product kernels read is put in order first: every operand as
+// [heads][N_pad] rows, queries by mask slot and keys by tile, pad rows zeros,
+// so that each tile is a plain 128-row box.  (Read through 4-D boxes of the
+// natural layout, the same tiles kept the copy engine behind the products:
+// 3180 instead of 2406 cycles a tile pair in backward_q at 21 x 30 x 52.)
+// A copy that is not needed has a null pointer.  d/8 lanes per row; blockIdx.y
+// is the head.  IN_F32: dout and out are fp32 (else bf16); dO is rounded to
+// bf16 first and D_i taken from the rounded values, the ones the products
+// use.  HBM-bound: 2 to 8 bf16 rows read and up to 4 written per token.
+struct RowCopies {
+    uint4 *q, *dout, *k, *v;
+};
+
 template <int D, bool IN_F32>
 __global__ void __launch_bounds__(256)
 backward_rows_kernel(const Geom G, const uint8_t* __restrict__ mask, const void* __restrict__ out,
                      const void* __restrict__ dout, const float* __restrict__ lse, const uint4* __restrict__ q,
-                     float4* __restrict__ rows, uint32_t* __restrict__ q_copy, uint32_t* __restrict__ do_copy)
+                     const uint4* __restrict__ k, const uint4* __restrict__ v, float4* __restrict__ rows, const RowCopies copy)
 {
-    const int lane = threadIdx.x & 31;
-    const size_t p = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);     // head, slot, row
-    if (p >= (size_t)G.G * G.N_pad) return;
-    const int g = (int)(p / G.N_pad);
-    const int in = (int)(p - (size_t)g * G.N_pad);
+    constexpr int LPR = D / 8;                                        // lanes per row
+    const int g = blockIdx.y, sub = threadIdx.x % LPR;
+    const int in = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;      // row of the head; N_pad is a multiple of 128
+    const size_t p = (size_t)g * G.N_pad + in;
     const int slot = in >> 7;
-    int t, tr, tc, i = in & 127;
+    int t, tr, tc;
     tile_coords(G, slot, t, tr, tc);
-    bool ok = true;
-    if (G.qsort) {
-        int l = reinterpret_cast<const uint16_t*>(mask + G.off_group)[p];
-        if (l >= 128 * G.nTh) {                                       // caller memory: recorded, the row left out
-            if (lane == 0) atomicOr(&g_tra_error, TRA_ERRBIT_CHECK);
-            l = 0;
-            ok = false;
-        }
-        tr = l >> 7;
-        i = l & 127;
+    // the token of tile row i in tile row tr of this slot's tile column and frame
+    auto token = [&](int tr, int i, int& h, int& w, int& trow) -> bool {
+        h = tr * G.th + (i >> G.tw_log2);
+        w = tc * G.tw + (i & (G.tw - 1));
+        trow = ((t * G.nTh + tr) * G.nTw + tc) * 128 + i;
+        return h < G.H && w < G.W;
+    };
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    int h, w, trow;
+    if (copy.k) {
+        const bool ok = token(tr, in & 127, h, w, trow);
+        const size_t at = ok ? io_row(G, g, t, h, w, trow) * LPR + sub : 0;
+        copy.k[p * LPR + sub] = ok ? __ldg(k + at) : zero;
+        copy.v[p * LPR + sub] = ok ? __ldg(v + at) : zero;
     }
-    const int h = tr * G.th + (i >> G.tw_log2), w = tc * G.tw + (i & (G.tw - 1));
-    ok = ok && h < G.H && w < G.W;
-    const int trow = ((t * G.nTh + tr) * G.nTw + tc) * 128 + i;       // tile-major row of the token
+    int qtr = tr, qi = in & 127;
+    bool named = true;
+    if (G.qsort) {
+        const int l = reinterpret_cast<const uint16_t*>(mask + G.off_group)[p];
+        named = l < 128 * G.nTh;                                      // caller memory: recorded, the row left out
+        if (!named && sub == 0) atomicOr(&g_tra_error, TRA_ERRBIT_CHECK);
+        qtr = named ? l >> 7 : 0;
+        qi = named ? l & 127 : 0;
+    }
+    const bool ok = token(qtr, qi, h, w, trow) && named;
     const size_t src = ok ? io_row(G, g, t, h, w, trow) : 0;
-    constexpr int PAIRS = D / 64;                                     // bf16 pairs per lane
+    uint4 x = zero;                                                   // 8 elements of dO as bf16
     float d = 0.f;
+    if (ok) {
+        float o[8];
+        if constexpr (IN_F32) {
+            const float4* xs = static_cast<const float4*>(dout) + src * (D / 4) + 2 * sub;
+            const float4* os = static_cast<const float4*>(out) + src * (D / 4) + 2 * sub;
+            const float4 x0 = __ldg(xs), x1 = __ldg(xs + 1), o0 = __ldg(os), o1 = __ldg(os + 1);
+            x = make_uint4(pack_bf16x2(x0.x, x0.y), pack_bf16x2(x0.z, x0.w), pack_bf16x2(x1.x, x1.y), pack_bf16x2(x1.z, x1.w));
+            o[0] = o0.x; o[1] = o0.y; o[2] = o0.z; o[3] = o0.w; o[4] = o1.x; o[5] = o1.y; o[6] = o1.z; o[7] = o1.w;
+        } else {
+            x = __ldg(static_cast<const uint4*>(dout) + src * LPR + sub);
+            const uint4 ob = __ldg(static_cast<const uint4*>(out) + src * LPR + sub);
+            const uint32_t w4[4] = {ob.x, ob.y, ob.z, ob.w};
 #pragma unroll
-    for (int k = 0; k < PAIRS; ++k) {
-        const size_t at = src * (D / 2) + k * 32 + lane;
-        uint32_t bits = 0;
-        float o0 = 0.f, o1 = 0.f;
-        if (ok) {
-            if constexpr (IN_F32) {
-                const float2 x = static_cast<const float2*>(dout)[at], o = static_cast<const float2*>(out)[at];
-                bits = pack_bf16x2(x.x, x.y);
-                o0 = o.x;
-                o1 = o.y;
-            } else {
-                bits = static_cast<const uint32_t*>(dout)[at];
-                const uint32_t o = static_cast<const uint32_t*>(out)[at];
-                o0 = __uint_as_float(o << 16);
-                o1 = __uint_as_float(o & 0xffff0000u);
+            for (int i = 0; i < 4; ++i) {
+                o[2 * i] = __uint_as_float(w4[i] << 16);
+                o[2 * i + 1] = __uint_as_float(w4[i] & 0xffff0000u);
             }
         }
-        d = fmaf(__uint_as_float(bits << 16), o0, d);
-        d = fmaf(__uint_as_float(bits & 0xffff0000u), o1, d);
-        if (do_copy) do_copy[p * (D / 2) + k * 32 + lane] = bits;
-        if (q_copy) q_copy[p * (D / 2) + k * 32 + lane] = ok ? reinterpret_cast<const uint32_t*>(q)[at] : 0u;
-    }
+        const uint32_t x4[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (lane == 0) {
+        for (int i = 0; i < 4; ++i) {
+            d = fmaf(__uint_as_float(x4[i] << 16), o[2 * i], d);
+            d = fmaf(__uint_as_float(x4[i] & 0xffff0000u), o[2 * i + 1], d);
+        }
+    }
+    if (copy.dout) copy.dout[p * LPR + sub] = x;
+    if (copy.q) copy.q[p * LPR + sub] = ok ? __ldg(q + src * LPR + sub) : zero;
+#pragma unroll
+    for (int s = LPR / 2; s > 0; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
+    if (sub == 0) {
         int r = ok ? reinterpret_cast<const int32_t*>(mask + G.off_radius)[(size_t)g * G.N_pad + trow] : -1;
         float l2 = 0.f;
         if (ok) {
             l2 = lse[src] * 1.4426950408889634f;
             if (l2 == -INFINITY) { l2 = 0.f; r = -1; }                // a row that kept nothing
         }
-        rows[p] = make_float4(l2, ok ? d : 0.f, __int_as_float(h | (w << 8)), __int_as_float(r));
+        rows[p] = make_float4(l2, d, __int_as_float(h | (w << 8)), __int_as_float(r));
     }
 }
 
@@ -161,31 +179,40 @@ transpose_lists_kernel(const Geom G, const uint8_t* __restrict__ mask, uint32_t*
 }
 
 // ------------------------------------------------------------------ masks
-// Keep-bits of a query at (hq, wq) with half-width s over a key tile at (h0, w0)
-// with khv x kwv valid keys, as four 32-key words.
-template <int TWL, bool DISK>
-__device__ __forceinline__ void query_keep_bits(const Geom& G, int hq, int wq, int s, int h0, int w0, int khv, int kwv,
-                                                uint32_t (&m)[4])
+// the low n bits, 0 <= n <= 32 (PTX shifts by 32 or more give 0)
+__device__ __forceinline__ uint32_t low_bits(int n)
 {
-    constexpr int TW = 1 << TWL;
-    if constexpr (!DISK) {
-        row_keep_bits<TWL>(max(0, hq - s - h0), min(khv - 1, hq + s - h0), max(0, wq - s - w0), min(kwv - 1, wq + s - w0), m);
-    } else {
+    uint32_t r;
+    asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(0xffffffffu), "r"(n));
+    return ~r;
+}
+
+// The keys lo .. hi of a tile's 32 key rows or columns, as bits: those within s
+// of y (s < 0: none) among the n valid ones.
+__device__ __forceinline__ uint32_t kept_line(int y, int s, int n)
+{
+    return s < 0 ? 0u : low_bits(max(0, min(n, y + s + 1))) & ~low_bits(min(max(0, y - s), 32));
+}
+
+// Bit i of lane j's word goes to bit j of lane i's word.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t v, int lane)
+{
 #pragma unroll
-        for (int wd = 0; wd < 4; ++wd) {
-            uint32_t v = 0;
-#pragma unroll
-            for (int k = 0; k < 32 / TW; ++k) {
-                const int a = (wd * 32) / TW + k, dh = h0 + a - hq, thr = s * s - dh * dh;
-                if (a < khv && thr >= 0) {
-                    const int half = isqrt_floor(thr);
-                    const int lo = max(0, wq - half - w0), hi = min(kwv - 1, wq + half - w0);
-                    if (lo <= hi) v |= ((2u << hi) - (1u << lo)) << ((a * TW) & 31);
-                }
-            }
-            m[wd] = v;
-        }
+    for (int s = 16; s > 0; s >>= 1) {
+        const uint32_t m = s == 16 ? 0x0000ffffu : (s == 8 ? 0x00ff00ffu : (s == 4 ? 0x0f0f0f0fu : (s == 2 ? 0x33333333u : 0x55555555u)));
+        const uint32_t y = __shfl_xor_sync(0xffffffffu, v, s);
+        v = (lane & s) ? (v & ~m) | ((y & ~m) >> s) : (v & m) | ((y & m) << s);
     }
+    return v;
+}
+
+// x as the sum of three bf16 numbers (24 bits), in the first three of the eight
+// bf16 of a 16-byte chunk
+__device__ __forceinline__ uint4 split_bf16x3(float x)
+{
+    const float hi = __bfloat162float(__float2bfloat16(x));
+    const float mid = __bfloat162float(__float2bfloat16(x - hi));
+    return make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(x - hi - mid, 0.f), 0u, 0u);
 }
 
 // Stores 32 accumulator columns of one row, scaled.
@@ -219,16 +246,23 @@ __device__ __forceinline__ void store_cols32(void* base, bool bf16, size_t elem,
 //              fp32 and written back over S^T as bf16), then reads dP^T and
 //              writes dS^T over it.
 //   warp 8     TMA: K, V once, then the rings of Q and dO.
-//   warp 9     MMA issuer.  Each half of a slot is a chain of its own:
-//              {dV += P^T dO, S^T of slot j+1} once P^T of slot j is there, and
-//              {dK += dS^T Q, dP^T of slot j+1} once dS^T is; the groups of the
-//              two halves alternate, so one half's elementwise work runs
-//              under the other's products.  MMAs of one thread run in order,
-//              so S^T of j+1 overwrites P^T of j only after dV has read it, and
-//              dP^T of j+1 overwrites dS^T of j only after dK has.
-//   warps 10, 11  per slot, the 64 queries' lse and D_i and the keep-bits of
-//              all 128 keys into a two-stage ring (and whether all are set:
-//              such halves skip the masking).
+//   warp 9     MMA issuer.  Per slot j, two groups alternate with the two
+//              halves of the elementwise work: {dV += P^T dO, S^T of slot j+1}
+//              while dS^T of j is made, {dK += dS^T Q, dP^T of slot j+1} while
+//              P^T of j+1 is made.  MMAs of one thread run in order, so S^T of
+//              j+1 overwrites P^T of j only after dV has read it, and dP^T of
+//              j+1 overwrites dS^T of j only after dK has.
+//   warps 10, 11  per slot and half, the per-query data into a ring: planes of
+//              -lse and -D_i for the tensor core, what the keys need to know
+//              which queries keep them (square: a 64-bit word per key row
+//              and per key column, whose AND is a key's; disk: three numbers
+//              per query), and whether all pairs are kept (such halves skip
+//              the masking).
+// The products read shared memory at its full rate, so the elementwise work
+// keeps off it: lse and D_i vary along the columns, and fetching them per
+// column (and a mask word each) took 1536 cycles of that bandwidth per tile
+// pair.  Instead one more K step of the product adds them: a row of ones times
+// the number split into three bf16 parts (24 bits).
 // TMEM columns: S^T [0,128), dP^T [128,256), dV [256,256+D), dK [384,384+D).
 // P^T of warpgroup u: bf16 pairs in columns 64u .. 64u+31 (its own half of
 // S^T, so the other half's S^T is never overwritten early); dS^T likewise.
@@ -237,16 +271,24 @@ struct BwdKvCfg {
     static constexpr int PANEL = 128 * 128;
     static constexpr int NP = D / 64;
     static constexpr int TILE = NP * PANEL;
-    static constexpr int ST = 2;                            // Q and dO ring depth
     static constexpr int OFF_K = 0, OFF_V = TILE;
-    static constexpr int OFF_Q = 2 * TILE, OFF_DO = OFF_Q + ST * TILE;
-    static constexpr int OFF_META = OFF_DO + ST * TILE;     // [ST][2 halves]: -lse[64], -D[64], words[4][64]
-    static constexpr int META = 64 * 4 * 6;                 // bytes of a half
-    static constexpr int OFF_BARS = OFF_META + ST * 2 * META;
-    static constexpr int OFF_LIST = OFF_BARS + 32 * 8 + 64; // uint16 [list_cap]
+    static constexpr int OFF_RING = 2 * TILE;               // four tiles: Q and dO of two slots
+    static constexpr int MST = 3;                           // ring depth of the per-query data
+    static constexpr int OFF_ONE = OFF_RING + 4 * TILE;     // 128 rows of (1, 1, 1, 0, ..), 16 bytes each
+    static constexpr int OFF_META = OFF_ONE + 2048;         // [MST]: planes of -lse and -D, key ranges [2 halves][1024 bytes]
+    static constexpr int META = 3 * 2048;
+    static constexpr int OFF_ZERO = OFF_META + MST * META;  // a plane of zeros
+    static constexpr int OFF_BARS = OFF_ZERO + 2048;
+    static constexpr int OFF_LIST = OFF_BARS + 40 * 8 + 64; // uint16 [list_cap]
     static constexpr int THREADS = 384;
     static constexpr int REGS_SOFTMAX = 216, REGS_OTHER = 72;
     static int smem(int list_cap) { return OFF_LIST + ((list_cap * 2 + 15) & ~15) + 1024; }
+    // The ring tiles of slot j's Q and dO.  dO of a slot is done with half a step
+    // before its Q (dV comes before dK), and Q is needed half a step before
+    // dO, so Q of slot j + 2 goes where dO of slot j was and dO of j + 2 where
+    // Q of j was: either has a whole step to arrive.
+    __device__ static int q_tile(int j) { return (j & 1) * 2 + ((j >> 1) & 1); }
+    __device__ static int do_tile(int j) { return q_tile(j) ^ 1; }
 };
 
 template <int D, int TWL, bool DISK>
@@ -261,22 +303,20 @@ backward_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
     uint64_t* kv_full = bars;
-    uint64_t* q_full = bars + 1;                 // [ST]
-    uint64_t* q_empty = q_full + C::ST;
-    uint64_t* do_full = q_empty + C::ST;
-    uint64_t* do_empty = do_full + C::ST;
-    uint64_t* meta_full = do_empty + C::ST;      // [ST][2]
-    uint64_t* meta_empty = meta_full + 2 * C::ST;
-    uint64_t* s_full = meta_empty + 2 * C::ST;   // [2], as the following: one per half
-    uint64_t* dp_full = s_full + 2;
-    uint64_t* p_full = dp_full + 2;
+    uint64_t* r_full = bars + 1;                 // [4]: ring tiles
+    uint64_t* r_empty = r_full + 4;
+    uint64_t* meta_full = r_empty + 4;           // [MST][2 halves]
+    uint64_t* meta_empty = meta_full + 2 * C::MST;
+    uint64_t* s_full = meta_empty + 2 * C::MST;
+    uint64_t* dp_full = s_full + 1;
+    uint64_t* p_full = dp_full + 1;              // [2]: the first and the last 32 queries of each half
     uint64_t* ds_full = p_full + 2;
-    uint64_t* done = ds_full + 2;
-    int* misc = reinterpret_cast<int*>(bars + 32);
+    uint64_t* done = ds_full + 1;
+    int* misc = reinterpret_cast<int*>(bars + 40);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc);
     volatile int* s_abort = misc + 1;
     int* s_n = misc + 2;
-    int* s_all = misc + 4;                       // [ST][2]: every pair of the half is kept
+    int* s_all = misc + 4;                       // [MST][2]: every pair of the half is kept
     uint16_t* list = reinterpret_cast<uint16_t*>(smem + C::OFF_LIST);
 
     const int kt = blockIdx.x, g = blockIdx.y;
@@ -308,18 +348,19 @@ backward_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     if (tid == 32) {
         mbar_init(kv_full, 1);
-        for (int i = 0; i < C::ST; ++i) {
-            mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
-            mbar_init(&do_full[i], 1); mbar_init(&do_empty[i], 1);
-        }
-        for (int i = 0; i < 2 * C::ST; ++i) { mbar_init(&meta_full[i], 32); mbar_init(&meta_empty[i], 128); }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1); mbar_init(&dp_full[i], 1);
-            mbar_init(&p_full[i], 128); mbar_init(&ds_full[i], 128);
-        }
+        for (int i = 0; i < 4; ++i) { mbar_init(&r_full[i], 1); mbar_init(&r_empty[i], 1); }
+        for (int i = 0; i < 2 * C::MST; ++i) { mbar_init(&meta_full[i], 32); mbar_init(&meta_empty[i], 128); }
+        mbar_init(s_full, 1); mbar_init(dp_full, 1);
+        mbar_init(&p_full[0], 256); mbar_init(&p_full[1], 256); mbar_init(ds_full, 256);
         mbar_init(done, 1);
         *s_abort = 0;
         fence_barrier_init();
+    }
+    if (tid >= 128 && tid < 256) {
+        const uint4 one = make_uint4(0x3f803f80u, 0x00003f80u, 0u, 0u);
+        reinterpret_cast<uint4*>(smem + C::OFF_ONE)[tid - 128] = one;
+        reinterpret_cast<uint4*>(smem + C::OFF_ZERO)[tid - 128] = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();                            // generic writes -> tensor-core reads
     }
     if (warp == 9) { tmem_alloc(s_tmem, 512); tmem_relinquish(); }
     __syncthreads();
@@ -333,142 +374,164 @@ backward_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (warp == 8) {
             if (n > 0 && elect_one()) {
                 prefetch_tmap(&tm_q); prefetch_tmap(&tm_k); prefetch_tmap(&tm_v); prefetch_tmap(&tm_do);
-                int iss_q = 0, iss_do = 0;
-                auto load_q = [&](int j) -> bool {
-                    const int st = j % C::ST;
-                    if (j >= C::ST && !role_wait(&q_empty[st], ((j / C::ST) - 1) & 1, G.wait_ns, s_abort)) return false;
-                    mbar_arrive_expect_tx(&q_full[st], C::TILE);
+                auto load = [&](const CUtensorMap* tm, int j, int tile) -> bool {
+                    if (j >= 2 && !role_wait(&r_empty[tile], ((j >> 1) - 1) & 1, G.wait_ns, s_abort)) return false;
+                    mbar_arrive_expect_tx(&r_full[tile], C::TILE);
 #pragma unroll
                     for (int p = 0; p < C::NP; ++p)
-                        load_panel(smem + C::OFF_Q + st * C::TILE + p * C::PANEL, &tm_q, A.q_natural, G, p, g, list[j], &q_full[st]);
-                    ++iss_q;
-                    return true;
-                };
-                auto load_do = [&](int j) -> bool {
-                    const int st = j % C::ST;
-                    if (j >= C::ST && !role_wait(&do_empty[st], ((j / C::ST) - 1) & 1, G.wait_ns, s_abort)) return false;
-                    mbar_arrive_expect_tx(&do_full[st], C::TILE);
-#pragma unroll
-                    for (int p = 0; p < C::NP; ++p)
-                        load_panel(smem + C::OFF_DO + st * C::TILE + p * C::PANEL, &tm_do, A.do_natural, G, p, g, list[j], &do_full[st]);
-                    ++iss_do;
+                        load_panel(smem + C::OFF_RING + tile * C::TILE + p * C::PANEL, tm, G, p, g, list[j], &r_full[tile]);
                     return true;
                 };
                 mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
 #pragma unroll
                 for (int p = 0; p < C::NP; ++p) {
-                    load_panel(smem + C::OFF_K + p * C::PANEL, &tm_k, G.natural, G, p, g, kt, kv_full);
-                    load_panel(smem + C::OFF_V + p * C::PANEL, &tm_v, G.natural, G, p, g, kt, kv_full);
+                    load_panel(smem + C::OFF_K + p * C::PANEL, &tm_k, G, p, g, kt, kv_full);
+                    load_panel(smem + C::OFF_V + p * C::PANEL, &tm_v, G, p, g, kt, kv_full);
                 }
-                // dO's stage is free half a step before Q's of the same slot
-                for (int j = 0; j < n; ++j)
-                    if (!(j < C::ST ? load_q(j) && load_do(j) : load_do(j) && load_q(j))) break;
+                int loads = 0;                               // Q(0), dO(0), Q(1), ...
+                for (; loads < 2 * n; ++loads) {
+                    const int j = loads >> 1;
+                    if (!((loads & 1) ? load(&tm_do, j, C::do_tile(j)) : load(&tm_q, j, C::q_tile(j)))) break;
+                }
                 // copies still in flight must land before the CTA exits
                 mbar_wait(kv_full, 0, G.drain_ns);
-                for (int j = max(0, iss_q - C::ST); j < iss_q; ++j) mbar_wait(&q_full[j % C::ST], (j / C::ST) & 1, G.drain_ns);
-                for (int j = max(0, iss_do - C::ST); j < iss_do; ++j) mbar_wait(&do_full[j % C::ST], (j / C::ST) & 1, G.drain_ns);
+                for (int i = max(0, loads - 4); i < loads; ++i) {
+                    const int j = i >> 1;
+                    mbar_wait(&r_full[(i & 1) ? C::do_tile(j) : C::q_tile(j)], (j >> 1) & 1, G.drain_ns);
+                }
             }
         } else if (warp == 9) {
             if (n > 0 && elect_one()) {
-                constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 64, false);
+                constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, false);
                 constexpr uint32_t IDESC_G = idesc_bf16_f32(128, D, true);
                 const uint32_t sK = smem_u32(smem + C::OFF_K), sV = smem_u32(smem + C::OFF_V);
-                const uint32_t sQ = smem_u32(smem + C::OFF_Q), sD = smem_u32(smem + C::OFF_DO);
-                // A (keys) times B^T (the 64 queries of half u), both K-major
-                auto scores = [&](uint32_t col, uint32_t a, uint32_t b, int u) {
+                const uint32_t sR = smem_u32(smem + C::OFF_RING);
+                const uint32_t sOne = smem_u32(smem + C::OFF_ONE), sMeta = smem_u32(smem + C::OFF_META), sZero = smem_u32(smem + C::OFF_ZERO);
+                // A (keys) times B^T (queries), both K-major, plus 1 times the
+                // plane's number of each query
+                auto scores = [&](uint32_t col, uint32_t a, uint32_t b, uint32_t plane, uint64_t* full) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * C::PANEL + (kk & 3) * 32;
-                        mma_ss(tmem + col + u * 64, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off + u * 8192, 16, 1024),
-                               IDESC_S, kk > 0 ? 1u : 0u);
+                        mma_ss(tmem + col, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off, 16, 1024), IDESC_S, kk > 0 ? 1u : 0u);
+                    }
+                    mma_ss(tmem + col, smem_desc_plain(sOne, sZero - sOne, 128), smem_desc_plain(plane, sZero - plane, 128), IDESC_S, 1u);
+                    mma_commit(full);
+                };
+                // the bf16 pairs in quarter c of the two halves of `col` times their rows of b
+                auto accumulate = [&](uint32_t dst, uint32_t col, uint32_t b, int c, bool add) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int kk = (i >> 1) * 4 + c * 2 + (i & 1);
+                        mma_ts(tmem + dst, tmem + col + (kk >> 2) * 64 + (kk & 3) * 8,
+                               smem_desc_sw128(b + kk * 2048, C::PANEL, 1024), IDESC_G, (add || i > 0) ? 1u : 0u);
                     }
                 };
-                // the bf16 pairs in half u of `col` times the 64 rows of half u of b
-                auto accumulate = [&](uint32_t dst, uint32_t col, uint32_t b, int u, bool add) {
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ts(tmem + dst, tmem + col + u * 64 + kk * 8,
-                               smem_desc_sw128(b + u * 8192 + kk * 2048, C::PANEL, 1024), IDESC_G, (add || kk > 0) ? 1u : 0u);
-                };
-                bool ok = role_wait(kv_full, 0, G.wait_ns, s_abort) && role_wait(&q_full[0], 0, G.wait_ns, s_abort);
+                auto wait_q = [&](int j) -> bool { return role_wait(&r_full[C::q_tile(j)], (j >> 1) & 1, G.wait_ns, s_abort); };
+                auto wait_do = [&](int j) -> bool { return role_wait(&r_full[C::do_tile(j)], (j >> 1) & 1, G.wait_ns, s_abort); };
+                auto issue_s = [&](int j) { scores(COL_S, sK, sR + C::q_tile(j) * C::TILE, sMeta + j % C::MST * C::META, s_full); };
+                auto issue_dp = [&](int j) { scores(COL_DP, sV, sR + C::do_tile(j) * C::TILE, sMeta + j % C::MST * C::META + 2048, dp_full); };
+                bool ok = role_wait(&meta_full[0], 0, G.wait_ns, s_abort) && role_wait(&meta_full[1], 0, G.wait_ns, s_abort) &&
+                          role_wait(kv_full, 0, G.wait_ns, s_abort) && wait_q(0) && wait_do(0);
                 if (ok) {
                     tc_fence_after();
-                    for (int u = 0; u < 2; ++u) {
-                        scores(COL_S, sK, sQ, u);
-                        mma_commit(&s_full[u]);
-                    }
-                    ok = role_wait(&do_full[0], 0, G.wait_ns, s_abort);
-                }
-                if (ok) {
-                    for (int u = 0; u < 2; ++u) {
-                        scores(COL_DP, sV, sD, u);
-                        mma_commit(&dp_full[u]);
-                    }
+                    issue_s(0);
+                    issue_dp(0);
                 }
                 for (int j = 0; ok && j < n; ++j) {
-                    const int st = j % C::ST, sn = (j + 1) % C::ST;
+                    const int qt = C::q_tile(j), dt = C::do_tile(j);
                     const bool next = j + 1 < n;
-                    for (int u = 0; ok && u < 2; ++u) {
-                        ok = role_wait(&p_full[u], j & 1, G.wait_ns, s_abort);
-                        if (!ok) break;
-                        tc_fence_after();
-                        accumulate(COL_DV, COL_S, sD + st * C::TILE, u, j > 0 || u > 0);
-                        if (u == 1) mma_commit(&do_empty[st]);
-                        if (!next) continue;
-                        if (u == 0) ok = role_wait(&q_full[sn], ((j + 1) / C::ST) & 1, G.wait_ns, s_abort);
-                        if (!ok) break;
-                        scores(COL_S, sK, sQ + sn * C::TILE, u);
-                        mma_commit(&s_full[u]);
-                    }
-                    for (int u = 0; ok && u < 2; ++u) {
-                        ok = role_wait(&ds_full[u], j & 1, G.wait_ns, s_abort);
-                        if (!ok) break;
-                        tc_fence_after();
-                        accumulate(COL_DK, COL_DP, sQ + st * C::TILE, u, j > 0 || u > 0);
-                        if (u == 1) mma_commit(&q_empty[st]);
-                        if (!next) continue;
-                        if (u == 0) ok = role_wait(&do_full[sn], ((j + 1) / C::ST) & 1, G.wait_ns, s_abort);
-                        if (!ok) break;
-                        scores(COL_DP, sV, sD + sn * C::TILE, u);
-                        mma_commit(&dp_full[u]);
-                    }
+                    // what a group needs besides P^T or dS^T is waited for first:
+                    // a wait takes 100 to 200 cycles even when it is over
+                    if (next && !wait_q(j + 1)) break;
+                    if (!role_wait(&p_full[0], j & 1, G.wait_ns, s_abort)) break;
+                    tc_fence_after();
+                    accumulate(COL_DV, COL_S, sR + dt * C::TILE, 0, j > 0);
+                    if (!role_wait(&p_full[1], j & 1, G.wait_ns, s_abort)) break;
+                    tc_fence_after();
+                    accumulate(COL_DV, COL_S, sR + dt * C::TILE, 1, true);
+                    mma_commit(&r_empty[dt]);
+                    if (next) issue_s(j + 1);
+                    if (next && !wait_do(j + 1)) break;
+                    if (!role_wait(ds_full, j & 1, G.wait_ns, s_abort)) break;
+                    tc_fence_after();
+                    accumulate(COL_DK, COL_DP, sR + qt * C::TILE, 0, j > 0);
+                    accumulate(COL_DK, COL_DP, sR + qt * C::TILE, 1, true);
+                    mma_commit(&r_empty[qt]);
+                    if (next) issue_dp(j + 1);
                 }
                 // every issued MMA must finish before the results are read and TMEM is freed
                 mma_commit(done);
                 mbar_wait(done, 0, G.drain_ns);
             }
         } else {
-            // ------------------------------------------------ queries' lse, D_i and keep-bits
+            // ------------------------------------------------ queries' lse, D_i and kept keys
             const int half = warp - 10;
+            const float4* rows = A.rows + (size_t)g * G.nQ * 128 + half * 64 + lane;
+            const float unit = -1.f / G.scale_log2;          // lse in units of the raw scores, negated
+            float4 r0, r1;
+            if (n > 0) {
+                r0 = __ldg(rows + list[0] * 128);
+                r1 = __ldg(rows + list[0] * 128 + 32);
+            }
             for (int j = 0; j < n; ++j) {
-                const int st = j % C::ST, ring = st * 2 + half;
-                const int slot = list[j];
-                const float4* src = A.rows + ((size_t)g * G.nQ + slot) * 128 + half * 64 + lane;
-                const float4 r0 = __ldg(src), r1 = __ldg(src + 32);
-                const double decay = G.g[abs(slot / G.tiles_per_frame - tk)];
-                uint32_t m[2][4];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int pos = __float_as_int(x ? r1.z : r0.z), r = __float_as_int(x ? r1.w : r0.w);
-                    if (r >= 0)
-                        query_keep_bits<TWL, DISK>(G, pos & 255, (pos >> 8) & 255, min(halfwidth(r, decay), TRA_DISK_S_CLAMP), h0, w0, khv, kwv, m[x]);
-                    else
-                        m[x][0] = m[x][1] = m[x][2] = m[x][3] = 0u;
+                const int st = j % C::MST, ring = st * 2 + half;
+                const float4 x[2] = {r0, r1};
+                const double decay = G.g[abs(list[j] / G.tiles_per_frame - tk)];
+                if (j + 1 < n) {                             // the next slot's rows are on their way meanwhile
+                    r0 = __ldg(rows + list[j + 1] * 128);
+                    r1 = __ldg(rows + list[j + 1] * 128 + 32);
                 }
-                const bool all = __all_sync(0xffffffffu, (m[0][0] & m[0][1] & m[0][2] & m[0][3] & m[1][0] & m[1][1] & m[1][2] & m[1][3]) == 0xffffffffu);
-                bool got = true;
-                if (j >= C::ST) got = role_wait(&meta_empty[ring], ((j / C::ST) - 1) & 1, G.wait_ns, s_abort);
-                if (__any_sync(0xffffffffu, !got)) break;
-                float* f = reinterpret_cast<float*>(smem + C::OFF_META + ring * C::META);
-                uint32_t* wd = reinterpret_cast<uint32_t*>(f + 128);
-                f[lane] = -r0.x; f[lane + 32] = -r1.x;
-                f[64 + lane] = -r0.y; f[96 + lane] = -r1.y;
+                // square: the kept key rows and columns; disk: A, B, C of the test
+                // A + B a + C b <= -(a^2 + b^2) that key (a, b) makes of the query at
+                // (y, x), with A = y^2 + x^2 - s^2, B = -2y, C = -2x (integers
+                // below 2^23, exact in fp32)
+                uint32_t m[2][3];
+                bool all = true;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    wd[k * 64 + lane] = m[0][k];
-                    wd[k * 64 + lane + 32] = m[1][k];
+                for (int k = 0; k < 2; ++k) {
+                    const int pos = __float_as_int(x[k].z), r = __float_as_int(x[k].w);
+                    const int y = (pos & 255) - h0, xx = ((pos >> 8) & 255) - w0;
+                    const int s = r >= 0 ? min(halfwidth(r, decay), TRA_DISK_S_CLAMP) : -1;
+                    if constexpr (DISK) {
+                        const int fy = max(abs(y), abs(y - (G.th - 1))), fx = max(abs(xx), abs(xx - (TW - 1)));
+                        all = all && khv == G.th && kwv == TW && s >= 0 && fy * fy + fx * fx <= s * s;
+                        m[k][0] = __float_as_uint(s >= 0 ? (float)(y * y + xx * xx - s * s) : 4e6f);   // 4e6: above any -(B a + C b)
+                        m[k][1] = __float_as_uint((float)(-2 * y));
+                        m[k][2] = __float_as_uint((float)(-2 * xx));
+                    } else {
+                        m[k][0] = kept_line(y, s, khv);
+                        m[k][1] = kept_line(xx, s, kwv);
+                        all = all && m[k][0] == low_bits(G.th) && m[k][1] == low_bits(TW);
+                    }
+                }
+                all = __all_sync(0xffffffffu, all);
+                if (!DISK && !all) {                         // from a query's keys to a key's queries
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int wd = 0; wd < 2; ++wd) m[k][wd] = transpose_bits(m[k][wd], lane);
+                }
+                bool got = true;
+                if (j >= C::MST) got = role_wait(&meta_empty[ring], ((j / C::MST) - 1) & 1, G.wait_ns, s_abort);
+                if (__any_sync(0xffffffffu, !got)) break;
+                uint4* lse4 = reinterpret_cast<uint4*>(smem + C::OFF_META + st * C::META) + half * 64 + lane;
+                lse4[0] = split_bf16x3(x[0].x * unit);
+                lse4[32] = split_bf16x3(x[1].x * unit);
+                lse4[128] = split_bf16x3(-x[0].y);
+                lse4[160] = split_bf16x3(-x[1].y);
+                uint32_t* keys = reinterpret_cast<uint32_t*>(smem + C::OFF_META + st * C::META + 4096 + half * 1024);
+                if constexpr (DISK) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int wd = 0; wd < 3; ++wd) keys[wd * 64 + k * 32 + lane] = m[k][wd];
+                } else {
+#pragma unroll
+                    for (int wd = 0; wd < 2; ++wd) reinterpret_cast<uint2*>(keys)[wd * 32 + lane] = make_uint2(m[0][wd], m[1][wd]);
                 }
                 if (lane == 0) s_all[ring] = all ? 1 : 0;
+                fence_proxy_async_smem();                    // the planes are read by the tensor core
                 mbar_arrive(&meta_full[ring]);
             }
         }
@@ -479,53 +542,77 @@ backward_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int row = tid & 127;                           // key row = TMEM lane
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t colS = tmem + lane_base + COL_S + u * 64, colP = tmem + lane_base + COL_DP + u * 64;
-        const uint32_t lbit = 1u << lane;
         const f2_t sc2 = f2_pack(G.scale_log2, G.scale_log2);
-        bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            const int ring = (j % C::ST) * 2 + u;
-            bool got = role_wait(&meta_full[ring], (j / C::ST) & 1, G.wait_ns, s_abort);
-            got = got && role_wait(&s_full[u], j & 1, G.wait_ns, s_abort);
+        const int ka = row >> TWL, kb = row & (TW - 1);      // this key's row and column in the tile
+        const f2_t ka2 = f2_pack((float)ka, (float)ka), kb2 = f2_pack((float)kb, (float)kb);
+        const float kthr = ka < khv && kb < kwv ? -(float)(ka * ka + kb * kb) : -INFINITY;
+        // this key's kept queries of the half, fetched one slot ahead; P^T of slot
+        // j is handed over after the per-query data of slot j + 1 has been seen,
+        // so the MMA issuer need not wait for it
+        bool all_next = false;
+        uint2 keep_next = make_uint2(0u, 0u);
+        auto fetch_keep = [&](int j) -> bool {
+            const int ms = j % C::MST;
+            if (!role_wait(&meta_full[ms * 2 + u], (j / C::MST) & 1, G.wait_ns, s_abort)) return false;
+            all_next = s_all[ms * 2 + u] != 0;
+            if constexpr (!DISK) {                           // a kept key row and a kept key column
+                const uint2* lines = reinterpret_cast<const uint2*>(smem + C::OFF_META + ms * C::META + 4096 + u * 1024);
+                const uint2 r = lines[row >> TWL], c = lines[32 + (row & (TW - 1))];
+                keep_next = make_uint2(r.x & c.x, r.y & c.y);
+            }
+            return true;
+        };
+        bool ok = n == 0 || fetch_keep(0);
+        ok = __all_sync(0xffffffffu, ok);
+        for (int j = 0; ok && j < n; ++j) {
+            const int ring = (j % C::MST) * 2 + u;
+            const bool all = all_next;
+            const uint2 keep = keep_next;
+            bool got = j + 1 == n || fetch_keep(j + 1);
+            got = got && role_wait(s_full, j & 1, G.wait_ns, s_abort);
             if (__any_sync(0xffffffffu, !got)) { ok = false; break; }
             tc_fence_after();
             __syncwarp();
-            const ulonglong2* lse2 = reinterpret_cast<const ulonglong2*>(smem + C::OFF_META + ring * C::META);
-            const ulonglong2* dd2 = lse2 + 16;
-            const uint4* wd4 = reinterpret_cast<const uint4*>(lse2 + 32) + (warp & 3) * 16;
-            const bool all = s_all[ring] != 0;
             uint32_t v[2][32];
             tmem_ld32(colS, v[0]);
             tmem_ld32(colS + 32, v[1]);
             tmem_wait_ld();
             f2_t p[32];
+            const f2_t* disk = reinterpret_cast<const f2_t*>(smem + C::OFF_META + (j % C::MST) * C::META + 4096 + u * 1024);
+            // S^T already holds the score minus the log-sum-exp, in score units
+            auto probabilities = [&](auto masked) {
+                constexpr bool MASKED = decltype(masked)::value;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t pk[16];
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t pk[16];
+                    const uint32_t m = c ? keep.y : keep.x;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const ulonglong2 l = lse2[c * 8 + i];
-                    float x0, x1, x2, x3;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c][4 * i]), __uint_as_float(v[c][4 * i + 1])), sc2, l.x), x0, x1);
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c][4 * i + 2]), __uint_as_float(v[c][4 * i + 3])), sc2, l.y), x2, x3);
-                    if (!all) {
-                        const uint4 m = wd4[c * 8 + i];
-                        x0 = (m.x & lbit) ? x0 : -INFINITY;
-                        x1 = (m.y & lbit) ? x1 : -INFINITY;
-                        x2 = (m.z & lbit) ? x2 : -INFINITY;
-                        x3 = (m.w & lbit) ? x3 : -INFINITY;
+                    for (int i = 0; i < 16; ++i) {
+                        float x0, x1;
+                        f2_unpack(f2_mul(f2_pack(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])), sc2), x0, x1);
+                        if constexpr (MASKED && DISK) {
+                            float t0, t1;
+                            f2_unpack(f2_fma(disk[64 + c * 16 + i], kb2, f2_fma(disk[32 + c * 16 + i], ka2, disk[c * 16 + i])), t0, t1);
+                            x0 = t0 <= kthr ? x0 : -INFINITY;
+                            x1 = t1 <= kthr ? x1 : -INFINITY;
+                        } else if constexpr (MASKED) {
+                            x0 = (m >> (2 * i)) & 1u ? x0 : -INFINITY;
+                            x1 = (m >> (2 * i + 1)) & 1u ? x1 : -INFINITY;
+                        }
+                        x0 = ex2(x0);
+                        x1 = ex2(x1);
+                        p[c * 16 + i] = f2_pack(x0, x1);
+                        pk[i] = pack_bf16x2(x0, x1);
                     }
-                    x0 = ex2(x0); x1 = ex2(x1); x2 = ex2(x2); x3 = ex2(x3);
-                    p[c * 16 + 2 * i] = f2_pack(x0, x1);
-                    p[c * 16 + 2 * i + 1] = f2_pack(x2, x3);
-                    pk[2 * i] = pack_bf16x2(x0, x1);
-                    pk[2 * i + 1] = pack_bf16x2(x2, x3);
+                    tmem_st16(colS + c * 16, pk);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(&p_full[c]);
                 }
-                tmem_st16(colS + c * 16, pk);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&p_full[u]);
-            got = role_wait(&dp_full[u], j & 1, G.wait_ns, s_abort);
+            };
+            if (all) probabilities(std::false_type{});
+            else probabilities(std::true_type{});
+            got = role_wait(dp_full, j & 1, G.wait_ns, s_abort);
             if (__any_sync(0xffffffffu, !got)) { ok = false; break; }
             tc_fence_after();
             __syncwarp();
@@ -533,22 +620,19 @@ backward_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tmem_ld32(colP + 32, v[1]);
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < 2; ++c) {                    // dP^T already holds dP - D
                 uint32_t pk[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const ulonglong2 dd = dd2[c * 8 + i];
-                    float x0, x1, x2, x3;
-                    f2_unpack(f2_mul(p[c * 16 + 2 * i], f2_add(f2_pack(__uint_as_float(v[c][4 * i]), __uint_as_float(v[c][4 * i + 1])), dd.x)), x0, x1);
-                    f2_unpack(f2_mul(p[c * 16 + 2 * i + 1], f2_add(f2_pack(__uint_as_float(v[c][4 * i + 2]), __uint_as_float(v[c][4 * i + 3])), dd.y)), x2, x3);
-                    pk[2 * i] = pack_bf16x2(x0, x1);
-                    pk[2 * i + 1] = pack_bf16x2(x2, x3);
+                for (int i = 0; i < 16; ++i) {
+                    float x0, x1;
+                    f2_unpack(f2_mul(p[c * 16 + i], f2_pack(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1]))), x0, x1);
+                    pk[i] = pack_bf16x2(x0, x1);
                 }
                 tmem_st16(colP + c * 16, pk);
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&ds_full[u]);
+            mbar_arrive(ds_full);
             mbar_arrive(&meta_empty[ring]);
         }
         // warpgroup 0 writes dV, warpgroup 1 dK; a key tile that no slot lists gets zeros
@@ -636,17 +720,16 @@ backward_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     volatile int* s_abort = misc + 1;
 
     const int slot = blockIdx.x, g = blockIdx.y;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5;
     const int ts = slot / G.tiles_per_frame;
     int n = reinterpret_cast<const int32_t*>(A.mask + G.off_count)[(size_t)g * G.nQ + slot];
     if (n < 0 || n > G.list_cap) n = 0;          // recorded by transpose_lists
     const uint16_t* list = reinterpret_cast<const uint16_t*>(A.mask + G.off_list) + ((size_t)g * G.nQ + slot) * G.list_cap;
     // a listed tile out of reach (recorded by transpose_lists) is replaced by
     // the slot's own tile with every pair masked
-    auto entry = [&](int j, bool& reach) -> int {
+    auto entry = [&](int j) -> int {
         const int e = __ldg(list + j) & 0x7fff;
-        reach = e < G.nQ && abs(e / G.tiles_per_frame - ts) <= G.rte;
-        return reach ? e : slot;
+        return e < G.nQ && abs(e / G.tiles_per_frame - ts) <= G.rte ? e : slot;
     };
 
     if (tid == 32) {
@@ -673,25 +756,24 @@ backward_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 mbar_arrive_expect_tx(q_full, 2 * C::TILE);
 #pragma unroll
                 for (int p = 0; p < C::NP; ++p) {
-                    load_panel(smem + C::OFF_Q + p * C::PANEL, &tm_q, A.q_natural, G, p, g, slot, q_full);
-                    load_panel(smem + C::OFF_DO + p * C::PANEL, &tm_do, A.do_natural, G, p, g, slot, q_full);
+                    load_panel(smem + C::OFF_Q + p * C::PANEL, &tm_q, G, p, g, slot, q_full);
+                    load_panel(smem + C::OFF_DO + p * C::PANEL, &tm_do, G, p, g, slot, q_full);
                 }
                 int iss_k = 0, iss_v = 0;
                 for (int j = 0; j < n; ++j) {
-                    bool reach;
-                    const int kt = entry(j, reach);
+                    const int kt = entry(j);
                     const int ks = j % C::KST, vs = j % C::VST;
                     if (j >= C::KST && !role_wait(&k_empty[ks], ((j / C::KST) - 1) & 1, G.wait_ns, s_abort)) break;
                     mbar_arrive_expect_tx(&k_full[ks], C::TILE);
 #pragma unroll
                     for (int p = 0; p < C::NP; ++p)
-                        load_panel(smem + C::OFF_K + ks * C::TILE + p * C::PANEL, &tm_k, G.natural, G, p, g, kt, &k_full[ks]);
+                        load_panel(smem + C::OFF_K + ks * C::TILE + p * C::PANEL, &tm_k, G, p, g, kt, &k_full[ks]);
                     ++iss_k;
                     if (j >= C::VST && !role_wait(&v_empty[vs], ((j / C::VST) - 1) & 1, G.wait_ns, s_abort)) break;
                     mbar_arrive_expect_tx(&v_full[vs], C::TILE);
 #pragma unroll
                     for (int p = 0; p < C::NP; ++p)
-                        load_panel(smem + C::OFF_V + vs * C::TILE + p * C::PANEL, &tm_v, G.natural, G, p, g, kt, &v_full[vs]);
+                        load_panel(smem + C::OFF_V + vs * C::TILE + p * C::PANEL, &tm_v, G, p, g, kt, &v_full[vs]);
                     ++iss_v;
                 }
                 mbar_wait(q_full, 0, G.drain_ns);
@@ -759,15 +841,27 @@ backward_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const f2_t nd2 = f2_pack(-meta.y, -meta.y);
         constexpr int KR = 64 >> TWL;                        // key rows of a half tile
         constexpr int CP = TW / 2;                           // column pairs of a key row
+        // The list's entries come one tile ahead (a load from global memory and
+        // the divisions and fp64 half-width of a tile took 1200 of 3250 cycles
+        // in front of each tile): coordinates by multiplication, exact since
+        // x < 2^15 and the product's error, x / n 2^-22, is below the 0.5 / n to
+        // the next integer; the half-width only when the key frame changes.
+        const float inv_tpf = 1.f / (float)G.tiles_per_frame, inv_ntw = 1.f / (float)G.nTw;
+        int e_next = n > 0 ? __ldg(list) & 0x7fff : 0;
+        int s_frame = -1, s = 0;
         bool ok = true;
         for (int j = 0; j < n; ++j) {
-            bool reach;
-            const int kt = entry(j, reach);
-            int tk, trk, tck;
-            tile_coords(G, kt, tk, trk, tck);
+            const int e = e_next;
+            if (j + 1 < n) e_next = __ldg(list + j + 1) & 0x7fff;
+            const int tk = (int)(((float)e + 0.5f) * inv_tpf), rem = e - tk * G.tiles_per_frame;
+            const int trk = (int)(((float)rem + 0.5f) * inv_ntw), tck = rem - trk * G.nTw;
+            const bool reach = e < G.nQ && abs(tk - ts) <= G.rte;
+            if (tk != s_frame) {
+                s_frame = tk;
+                s = reach && rq >= 0 ? min(halfwidth(rq, G.g[abs(tk - ts)]), TRA_DISK_S_CLAMP) : 0;
+            }
             const int h0 = trk * G.th + u * KR, w0 = tck * TW;
             const int khv = min(KR, G.H - h0), kwv = min(TW, G.W - w0);   // khv may be <= 0: a half past the grid's edge
-            const int s = rq >= 0 ? min(halfwidth(rq, G.g[abs(tk - ts)]), TRA_DISK_S_CLAMP) : 0;
             int a_lo = max(0, hq - s - h0), a_hi = min(khv - 1, hq + s - h0);
             const int b_lo = max(0, wq - s - w0), b_hi = min(kwv - 1, wq + s - w0);
             if (rq < 0 || !reach) { a_lo = 1; a_hi = 0; }

@@ -261,6 +261,16 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
            (1ull << 46) | (2ull << 61);
 }
 
+// The same without swizzling, K-major: 8-row x 16-byte core matrices of 128
+// contiguous bytes, 8-row groups SBO apart, 16-byte K chunks LBO apart.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) |
+           ((uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32) |
+           (1ull << 46);
+}
+
 // ----------------------------------------------------------------- math
 __device__ __forceinline__ float ex2(float x)
 {

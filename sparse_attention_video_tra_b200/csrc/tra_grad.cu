@@ -23,30 +23,31 @@ extern "C" tra_status tra_attention_lse(tra_plan plan, const void* q, const void
 namespace {
 
 // The workspace of tra_attention_backward: row data, the tile bitmaps, and the
-// copies of dO and Q in mask-slot order.  dO is copied unless the kernels can
-// read the caller's rows as they are (natural layout, bf16, no query groups):
-// fp32 rows need rounding, grouped rows reordering, and tile-major pad rows
-// must be zeros for the products.
+// operands in plain row order where the caller's are not: Q, K and V from the
+// natural layout, Q with query groups, and dO always (it may be fp32, and its
+// tile-major pad rows must be zeros for the products).
 struct BwdLayout {
-    bool copy_do, copy_q;
+    bool copy_q, copy_kv;                    // dO always has its copy
     int bw;
-    size_t off_bits, bits_bytes, off_do, off_q, total;
+    size_t off_bits, bits_bytes, off_do, off_q, off_k, off_v, total;
 };
 
 BwdLayout backward_layout(tra_plan plan)
 {
     const tra::Geom& G = plan->geom;
     BwdLayout L;
-    L.copy_q = G.qsort != 0;
-    L.copy_do = L.copy_q || !G.natural || !(plan->flags & TRA_FLAG_OUT_BF16);
+    L.copy_kv = G.natural != 0;
+    L.copy_q = G.natural || G.qsort;
     L.bw = tra::reach_words(G);
-    const size_t rows = (size_t)G.G * G.N_pad;
+    const size_t rows = (size_t)G.G * G.N_pad, tile_rows = rows * G.D * 2;
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     L.off_bits = up(rows * sizeof(float4));
     L.bits_bytes = (size_t)G.G * G.nQ * L.bw * 4;
     L.off_do = up(L.off_bits + L.bits_bytes);
-    L.off_q = up(L.off_do + (L.copy_do ? rows * G.D * 2 : 0));
-    L.total = up(L.off_q + (L.copy_q ? rows * G.D * 2 : 0));
+    L.off_q = up(L.off_do + tile_rows);
+    L.off_k = up(L.off_q + (L.copy_q ? tile_rows : 0));
+    L.off_v = up(L.off_k + (L.copy_kv ? tile_rows : 0));
+    L.total = up(L.off_v + (L.copy_kv ? tile_rows : 0));
     return L;
 }
 
@@ -96,13 +97,13 @@ extern "C" tra_status tra_attention_backward(tra_plan plan, const void* q, const
     const tra::Geom& G = plan->geom;
     const bool bf16 = (plan->flags & TRA_FLAG_OUT_BF16) != 0;
     uint8_t* ws = (uint8_t*)workspace;
-    uint8_t* do_copy = L.copy_do ? ws + L.off_do : nullptr;
-    uint8_t* q_copy = L.copy_q ? ws + L.off_q : nullptr;
+    const tra::RowCopies copy = {L.copy_q ? (uint4*)(ws + L.off_q) : nullptr, (uint4*)(ws + L.off_do),
+                                 L.copy_kv ? (uint4*)(ws + L.off_k) : nullptr, L.copy_kv ? (uint4*)(ws + L.off_v) : nullptr};
     const uint64_t rows = (uint64_t)G.G * G.N_pad;
     CUtensorMap mq, mk, mv, md;
-    if (!make_input_map(&mk, k, G) || !make_input_map(&mv, v, G)) return TRA_ERR_CUDA;
-    if (!(q_copy ? make_row_map(&mq, q_copy, rows, G.D) : make_input_map(&mq, q, G))) return TRA_ERR_CUDA;
-    if (!(do_copy ? make_row_map(&md, do_copy, rows, G.D) : make_input_map(&md, dout, G))) return TRA_ERR_CUDA;
+    if (!make_row_map(&mq, copy.q ? copy.q : q, rows, G.D) || !make_row_map(&mk, copy.k ? copy.k : k, rows, G.D) ||
+        !make_row_map(&mv, copy.v ? copy.v : v, rows, G.D) || !make_row_map(&md, copy.dout, rows, G.D))
+        return TRA_ERR_CUDA;
 
     cudaStream_t st = (cudaStream_t)stream;
     tra::BwdArgs A;
@@ -110,17 +111,14 @@ extern "C" tra_status tra_attention_backward(tra_plan plan, const void* q, const
     A.rows = (const float4*)ws;
     A.bits = (const uint32_t*)(ws + L.off_bits);
     A.bw = L.bw;
-    A.q_natural = G.natural && !q_copy;
-    A.do_natural = G.natural && !do_copy;
     A.out_bf16 = bf16 ? 1 : 0;
     A.dq = dq; A.dk = dk; A.dv = dv;
     A.grad_scale = (float)(1.0 / std::sqrt((double)G.D));
 
     if (cudaMemsetAsync(ws + L.off_bits, 0, L.bits_bytes, st) != cudaSuccess) return TRA_ERR_CUDA;
-    const unsigned row_blocks = (unsigned)((rows + 7) / 8);
+    const dim3 row_grid(G.N_pad * (G.D / 8) / 256, G.G);
     auto go = [&](auto kern) {
-        kern<<<row_blocks, 256, 0, st>>>(G, A.mask, out, dout, lse, (const uint4*)q, (float4*)ws, (uint32_t*)q_copy,
-                                         (uint32_t*)do_copy);
+        kern<<<row_grid, 256, 0, st>>>(G, A.mask, out, dout, lse, (const uint4*)q, (const uint4*)k, (const uint4*)v, (float4*)ws, copy);
     };
     if (G.D == 64) bf16 ? go(tra::backward_rows_kernel<64, false>) : go(tra::backward_rows_kernel<64, true>);
     else bf16 ? go(tra::backward_rows_kernel<128, false>) : go(tra::backward_rows_kernel<128, true>);
