@@ -279,6 +279,7 @@ class Plan:
         self.handle = tra_plan_create(T, H, W, heads, d, a, b, gamma, Rt, Bmin, flags)
         self.flags = flags
         self.info = tra_plan_query(self.handle)
+        self._cache_info = None
         self.params = dict(T=T, H=H, W=W, heads=heads, d=d, a=a, b=b, gamma=gamma, Rt=Rt, Bmin=Bmin)
 
     def close(self):
@@ -429,7 +430,8 @@ class Plan:
     def _on_device(self, *tensors):
         """All tensors on one device, which has to be the current one: the launch goes to its stream."""
         import torch
-        if len({x.device for x in tensors}) != 1 or tensors[0].device.index != torch.cuda.current_device():
+        current = torch.cuda.current_device()
+        if any(x.get_device() != current for x in tensors):
             raise ValueError(f"tensors on {sorted({str(x.device) for x in tensors})}; expected all on the current "
                              f"device, cuda:{torch.cuda.current_device()}")
 
@@ -465,10 +467,17 @@ class Plan:
         return dq, dk, dv
 
     # -- keys and values held in 8 bits
+    @property
+    def cache_info(self) -> CacheInfo:
+        """Sizes and offsets of this plan's cache (tra_cache_query)."""
+        if self._cache_info is None:
+            self._cache_info = tra_cache_query(self.handle)
+        return self._cache_info
+
     def new_cache(self, device="cuda"):
         """The 8-bit cache of this plan's grid and heads, nothing stored yet."""
         import torch
-        return torch.empty(tra_cache_query(self.handle).cache_bytes, dtype=torch.uint8, device=device)
+        return torch.empty(self.cache_info.cache_bytes, dtype=torch.uint8, device=device)
 
     def new_cache_workspace(self, n_frames, device="cuda"):
         """Workspace of cache_attention for up to n_frames query frames."""
@@ -478,15 +487,15 @@ class Plan:
     def cache_views(self, cache):
         """(k codes, v codes [heads, n_tiles, 128, d] float8_e4m3fn, k scale, v scale [heads, n_tiles] fp32)."""
         import torch
-        i, c = self.info, tra_cache_query(self.handle)
-
-        def codes(off):
-            return cache[off:off + i.heads * i.N_pad * i.d].view(torch.float8_e4m3fn).view(i.heads, i.n_tiles, 128, i.d)
-
-        def scale(off):
-            return cache[off:off + i.heads * i.n_tiles * 4].view(torch.float32).view(i.heads, i.n_tiles)
-
-        return codes(c.off_k), codes(c.off_v), scale(c.off_k_scale), scale(c.off_v_scale)
+        i, c = self.info, self.cache_info
+        self._buffer(cache, torch.uint8, c.cache_bytes, "cache")
+        cache = cache.view(-1)[:c.cache_bytes]
+        codes, scale = cache.view(torch.float8_e4m3fn), cache.view(torch.float32)
+        shape, strides = (i.heads, i.n_tiles, 128, i.d), (i.N_pad * i.d, 128 * i.d, i.d, 1)
+        first = cache.storage_offset()
+        return (codes.as_strided(shape, strides, first + c.off_k), codes.as_strided(shape, strides, first + c.off_v),
+                scale.as_strided(shape[:2], (i.n_tiles, 1), (first + c.off_k_scale) // 4),
+                scale.as_strided(shape[:2], (i.n_tiles, 1), (first + c.off_v_scale) // 4))
 
     def _frames(self, x, name) -> int:
         """How many frames of this plan's rows [heads, rows, d] x holds."""

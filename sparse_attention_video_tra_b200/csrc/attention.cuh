@@ -404,7 +404,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // ------------------------------------------------ TMA producers: Q_A, Q_B and the K ring
         // (warp 8), the V ring (warp 11); each walks the merged list on its own
         const bool isK = warp == C::WARP_LOAD;
-        if (lane == 0 && n > 0) {
+        if (n > 0 && elect_one()) {
             if (isK) {
                 prefetch_tmap(&tm_q); prefetch_tmap(&tm_k);
             } else {
@@ -455,7 +455,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // tile k only after s_full of tile k, whose commit covers every earlier
         // MMA of this thread, the PV of tile k-1 included.
         const int w = warp - C::WARP_MMA;
-        if (lane == 0 && n > 0) {
+        if (n > 0 && elect_one()) {
             constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, false);
             constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
             const uint32_t sQa = smem_u32(sQ) + w * C::TILE, sKa = smem_u32(sK), sVa = smem_u32(sV);
