@@ -10,6 +10,7 @@
 #pragma once
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "pipeline.cuh"
 
@@ -365,6 +366,411 @@ token_attention_kernel(const Geom G, const CacheView C, const uint4* __restrict_
         if (out_bf16) static_cast<__nv_bfloat16*>(out)[row * D + tid] = __float2bfloat16(val);
         else static_cast<float*>(out)[row * D + tid] = val;
         if (tid == 0) lse[row] = lc > 0.f ? (mc + log2f(lc)) * 0.69314718055994531f : -INFINITY;
+    }
+    if (csize > 1) cluster.sync();                           // the others' shared memory stays until it has been read
+}
+
+// ------------------------------------------------------------------ token groups
+// The same for many tokens: 16 places of the token list at a time as the rows
+// of mma.m16n8k16, so that a key's codes are fetched and converted once
+// for 16 queries (measured against one token at a time in the launch code).
+// One cluster of CTAs of 8 warps per (group, head).  The cached frames in reach
+// of any of the group's tokens are cut into granules of 16 keys that lie
+// together in the cache (16 rows of a tile: 16/w x w keys, w = min(tile_w, 16));
+// each frame's granules over the union of the tokens' boxes are dealt out to
+// the warps of the cluster, and a granule that no token keeps is left after the
+// mask test.  A warp's work on a granule:
+//   S = Q K^T   two 8-key column tiles, d/16 K steps.  The order of the d
+//               elements along K is free as long as Q and K agree: lane c of a
+//               quad takes the 16-code chunks c (and c + 4), word by word.
+//   softmax     running maximum per row (raised when exceeded by 2^8) and sum
+//               of the unrounded P; the weights of V are split into two f16
+//               parts, so nothing is rounded beyond 2^-22.
+//   O += P V    d/8 column tiles.  Column n of tile j is the d element
+//               (d/8) n + j, so the lane needs byte j of four key rows, and each
+//               pair of keys is one byte permute of two words.
+// The products run in f16, which holds every code, and one instruction turns two
+// codes into f16.  Q is scaled by a power of two per row to at most 2^15 (its 8
+// bits stay exact down to 2^-28 of the row's largest element; below, the error
+// is 2^-40 of that).  O has a frame of its own: the weights that multiply
+// codes are P times the V scale over 2^mv, kept below 2^15 by raising mv.
+__device__ __forceinline__ uint32_t codes_to_f16x2(uint32_t x)       // codes in bytes 0 and 1
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+struct GranuleFrame {
+    int y0, y1, x0, x1;          // granule rows and columns, first and last (none: y1 < y0)
+};
+
+constexpr int GROUP = 16, GROUP_WARPS = 8, GROUP_FRAMES = 64;
+
+template <int D>
+constexpr int group_smem_bytes() { return GROUP_WARPS * GROUP * D * 4; }
+
+template <int D, bool DISK>
+__global__ void __launch_bounds__(32 * GROUP_WARPS)
+token_group_kernel(const Geom G, const CacheView C, const uint32_t* __restrict__ q, const int32_t* __restrict__ token,
+                   const int32_t* __restrict__ radius, int n, int cached, int csize, void* __restrict__ out, int out_bf16,
+                   float* __restrict__ lse)
+{
+    namespace cg = cooperative_groups;
+    constexpr int KS = D / 16, NT = D / 8, CH = D / 64;      // K steps, column tiles of O, K chunks per lane and key
+    extern __shared__ __align__(16) float group_dyn[];
+    float (*s_o)[GROUP][D] = reinterpret_cast<float (*)[GROUP][D]>(group_dyn);      // [warps][GROUP][D]
+    __shared__ float s_m[GROUP_WARPS][GROUP], s_l[GROUP_WARPS][GROUP];
+    __shared__ float s_ml[GROUP][2];                         // of the CTA, for the cluster
+    __shared__ int s_half[GROUP][TRA_MAX_RT_EFF + 1];        // half-widths by |dt|; -1: keeps none
+    __shared__ int s_t[GROUP], s_h[GROUP], s_w[GROUP], s_r[GROUP];
+    __shared__ int s_lo, s_hi;
+    __shared__ GranuleFrame s_frame[GROUP_FRAMES];
+
+    const int groups = (n + GROUP - 1) / GROUP;
+    const int unit = blockIdx.x / csize, rank = blockIdx.x - unit * csize;
+    const int g = unit / groups, first = (unit - g * groups) * GROUP;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int area = G.H * G.W;
+
+    // ---- the group's tokens: place, half-widths, the frames any of them reaches
+    if (warp == 0) {
+        int t = -1, lo = 0x7fffffff, hi = 0;
+        if (lane < GROUP) {
+            const int i = first + lane;
+            const int tok = i < n ? token[i] : -1;
+            int r = -1, h = 0, w = 0;
+            if (tok >= G.N) {
+                if (rank == 0) atomicOr(&g_tra_error, TRA_ERRBIT_CHECK);
+            } else if (tok >= 0) {
+                r = radius[(size_t)g * n + i];
+                t = tok / area;
+                h = (tok - t * area) / G.W;
+                w = tok - t * area - h * G.W;
+                if (r >= 0) {
+                    lo = max(0, t - G.rte);
+                    hi = min(cached, t + G.rte + 1);
+                }
+            }
+            s_t[lane] = t;                                   // -1: an unused place
+            s_h[lane] = h;
+            s_w[lane] = w;
+            s_r[lane] = r;
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if (lane == 0) {
+            s_lo = lo;
+            s_hi = hi;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < GROUP * (G.rte + 1); i += 32 * GROUP_WARPS) {
+        const int r = s_r[i & (GROUP - 1)], d = i / GROUP;
+        s_half[i & (GROUP - 1)][d] = r >= 0 ? min(halfwidth(r, G.g[d]), TRA_DISK_S_CLAMP) : -1;
+    }
+    __syncthreads();
+    const int f_lo = s_lo, f_hi = max(s_lo == 0x7fffffff ? 0 : s_lo, s_hi);
+
+    // ---- this lane's rows r0, r0 + 8 of the group and its share of Q
+    const int c = lane & 3, r0 = lane >> 2;
+    uint32_t qa[KS][4];
+    float q_unit[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int i = first + r0 + 8 * x;
+        const bool ok = i < n && s_t[r0 + 8 * x] >= 0;
+        const uint4* src = reinterpret_cast<const uint4*>(q + ((size_t)g * n + (ok ? i : 0)) * (D / 2));
+        uint32_t w[CH][8], most = 0;                         // the lane's d elements and their largest magnitude (bf16 bits)
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            // d elements 16 (c + 4k) .. + 15: K steps 4k .. 4k + 3
+            const uint4 a = __ldg(src + 2 * (c + 4 * k)), b = __ldg(src + 2 * (c + 4 * k) + 1);
+            const uint32_t w8[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                w[k][s] = ok ? w8[s] : 0u;
+                most = max(most, max(w[k][s] & 0x7fffu, (w[k][s] >> 16) & 0x7fffu));
+            }
+        }
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        // 2^(14 - E) for a largest element of 1.f * 2^E, within what fp32 can undo
+        const int shift = min(max(14 - ((int)(most >> 7) - 127), -112), 126);
+        const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
+        q_unit[x] = __uint_as_float((uint32_t)(127 - shift) << 23);
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                qa[4 * k + (s >> 1)][(s & 1) * 2 + x] = pack_f16x2(__uint_as_float(w[k][s] << 16) * up, __uint_as_float(w[k][s] & 0xffff0000u) * up);
+    }
+    const int t0 = s_t[r0], t1 = s_t[r0 + 8], qh0 = s_h[r0], qh1 = s_h[r0 + 8], qw0 = s_w[r0], qw1 = s_w[r0 + 8];
+
+    float o[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};     // P is relative to 2^m
+    float mv[2] = {-INFINITY, -INFINITY};                       // O to 2^mv
+    const int gw_log2 = min(G.tw_log2, 4), gr_log2 = 4 - gw_log2;       // a granule: 2^gr_log2 x 2^gw_log2 keys
+    // A granule belongs to one of the cluster's warps by its number in the frame
+    // alone, not by the group's boxes: a row's sums run in the same order
+    // whatever tokens share its group.
+    const int warps = csize * GROUP_WARPS, wid = rank * GROUP_WARPS + warp;
+    const int row_granules = (G.nTw << G.tw_log2) >> gw_log2;
+    const float inv_row = 1.f / (float)row_granules;
+    const uint4* kc = reinterpret_cast<const uint4*>(C.k) + (size_t)g * G.N_pad * (D / 16);
+    const uint8_t* vc = C.v + (size_t)g * G.N_pad * D;
+
+    for (int fb = f_lo; fb < f_hi; fb += GROUP_FRAMES) {
+        // ---- the granules of up to 64 frames
+        const int nf = min(GROUP_FRAMES, f_hi - fb);
+        __syncthreads();
+        if (tid < nf) {
+            int y0 = 0x7fffffff, y1 = -1, x0 = 0x7fffffff, x1 = -1;
+            for (int i = 0; i < GROUP; ++i) {
+                const int dt = abs(fb + tid - s_t[i]);
+                if (s_t[i] < 0 || dt > G.rte) continue;
+                const int s = s_half[i][dt];
+                if (s < 0) continue;
+                y0 = min(y0, max(0, s_h[i] - s)); y1 = max(y1, min(G.H - 1, s_h[i] + s));
+                x0 = min(x0, max(0, s_w[i] - s)); x1 = max(x1, min(G.W - 1, s_w[i] + s));
+            }
+            s_frame[tid] = y1 < 0 ? GranuleFrame{0, -1, 0, -1}
+                                  : GranuleFrame{y0 >> gr_log2, y1 >> gr_log2, x0 >> gw_log2, x1 >> gw_log2};
+        }
+        __syncthreads();
+        // the walk over this warp's granules of the chunk: `at` is the next number in
+        // frame f, whose last one is `end`
+        int f = -1, at = 1, end = 0;
+        GranuleFrame F = {0, -1, 0, -1};
+        // The next granule with a kept key: its keep-bits, and its codes and scales on
+        // their way.  False at the end.  The loads of one granule run under the
+        // arithmetic of the one before.
+        uint32_t keep_n = 0;
+        uint4 kk_n[2][CH];
+        uint32_t vv_n[4][NT / 4];
+        float ks_n = 0.f, vs_n = 0.f;
+        auto fetch = [&]() -> bool {
+            for (;;) {
+                while (at > end) {
+                    if (++f >= nf) return false;
+                    F = s_frame[f];
+                    const int lo = F.y0 * row_granules + F.x0;
+                    end = F.y1 * row_granules + F.x1;
+                    // numbers of this warp are wid + 29 frame (an odd step) modulo the warps
+                    at = lo + ((wid + 29 * (fb + f) - lo) & (warps - 1));
+                }
+                const int gy = (int)(((float)at + 0.5f) * inv_row), gx = at - gy * row_granules;    // at < 2^16: exact
+                at += warps;
+                if (gx < F.x0 || gx > F.x1) continue;
+                const int h0 = gy << gr_log2, w0 = gx << gw_log2, frame = fb + f;
+                // ---- which of its 16 keys do the lane's two rows keep?  Key of score
+                // k of column tile j: 8 j + 2 c + k
+                const int dt0 = abs(frame - t0), dt1 = abs(frame - t1);
+                const int sa = t0 >= 0 && dt0 <= G.rte ? s_half[r0][dt0] : -1;
+                const int sb = t1 >= 0 && dt1 <= G.rte ? s_half[r0 + 8][dt1] : -1;
+                uint32_t keep = 0;                               // bit 4 x + 2 j + k: row x
+#pragma unroll
+                for (int jk = 0; jk < 4; ++jk) {
+                    const int key = 8 * (jk >> 1) + 2 * c + (jk & 1);
+                    const int h = h0 + (key >> gw_log2), w = w0 + (key & ((1 << gw_log2) - 1));
+                    const bool in = h < G.H && w < G.W;
+                    const int ah = abs(h - qh0), aw = abs(w - qw0), bh = abs(h - qh1), bw = abs(w - qw1);
+                    const bool ka = DISK ? sa >= 0 && ah * ah + aw * aw <= sa * sa : max(ah, aw) <= sa;
+                    const bool kb = DISK ? sb >= 0 && bh * bh + bw * bw <= sb * sb : max(bh, bw) <= sb;
+                    keep |= (in && ka ? 1u << jk : 0u) | (in && kb ? 16u << jk : 0u);
+                }
+                if (!__any_sync(0xffffffffu, keep != 0)) continue;
+                keep_n = keep;
+                const int tile = (frame * G.nTh + (h0 >> G.th_log2)) * G.nTw + (w0 >> G.tw_log2);
+                const size_t row = (size_t)tile * 128 + ((h0 & (G.th - 1)) << G.tw_log2) + (w0 & (G.tw - 1));
+                ks_n = __ldg(C.ks + (size_t)g * G.nQ + tile);
+                vs_n = __ldg(C.vs + (size_t)g * G.nQ + tile);
+                // ---- codes: K of keys r0 and r0 + 8 (chunks c, c + 4), V of keys 2c,
+                // 2c + 1, 2c + 8, 2c + 9 (the d/8 codes from (d/8) r0 on)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < CH; ++k) kk_n[j][k] = __ldg(kc + (row + 8 * j + r0) * (D / 16) + c + 4 * k);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint8_t* src = vc + (row + 2 * c + (i & 1) + 8 * (i >> 1)) * D + r0 * NT;
+                    if constexpr (NT == 16) {
+                        const uint4 a = __ldg(reinterpret_cast<const uint4*>(src));
+                        vv_n[i][0] = a.x; vv_n[i][1] = a.y; vv_n[i][2] = a.z; vv_n[i][3] = a.w;
+                    } else {
+                        const uint2 a = __ldg(reinterpret_cast<const uint2*>(src));
+                        vv_n[i][0] = a.x; vv_n[i][1] = a.y;
+                    }
+                }
+                return true;
+            }
+        };
+        bool more = fetch();
+        while (more) {
+            const uint32_t keep = keep_n;
+            const float ks = ks_n, vs = vs_n;
+            uint4 kk[2][CH];
+            uint32_t vv[4][NT / 4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int k = 0; k < CH; ++k) kk[j][k] = kk_n[j][k];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < NT / 4; ++k) vv[i][k] = vv_n[i][k];
+            more = fetch();
+            // ---- scores
+            float sc[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    const uint32_t w4[4] = {kk[j][k].x, kk[j][k].y, kk[j][k].z, kk[j][k].w};
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        mma_f16(sc[j], qa[4 * k + s], codes_to_f16x2(w4[s]), codes_to_f16x2(w4[s] >> 16));
+                }
+            }
+            // ---- softmax; p[x][2 j + k] of row x
+            float p[2][4];
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float unit = ks * q_unit[x] * G.scale_log2;
+#pragma unroll
+                for (int jk = 0; jk < 4; ++jk) {
+                    p[x][jk] = (keep >> (4 * x + jk)) & 1u ? sc[jk >> 1][2 * x + (jk & 1)] * unit : -INFINITY;
+                    mx[x] = fmaxf(mx[x], p[x][jk]);
+                }
+                mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
+                mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
+            }
+            const float lv = log2f(vs);                      // an integer
+            uint32_t ph[4], pl[4];
+            bool raise = false;
+            float al[2] = {1.f, 1.f};
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (mx[x] > m[x] + 8.f) {                    // -inf + 8: the first kept key
+                    l[x] *= m[x] == -INFINITY ? 0.f : ex2(m[x] - mx[x]);
+                    m[x] = mx[x];
+                }
+                // the weights' frame, raised where this granule's would pass 2^15
+                if (mx[x] > -INFINITY && m[x] + lv > mv[x] + 7.f) {
+                    al[x] = mv[x] == -INFINITY ? 0.f : ex2(mv[x] - (m[x] + lv));
+                    mv[x] = m[x] + lv;
+                    raise = true;
+                }
+                const float base = m[x] == -INFINITY ? 0.f : m[x];
+                const float wv = mx[x] > -INFINITY ? ex2(m[x] + lv - mv[x]) : 0.f;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float a = ex2(p[x][2 * j] - base), b = ex2(p[x][2 * j + 1] - base);
+                    l[x] += a + b;
+                    const float av = a * wv, bv = b * wv;
+                    const uint32_t hi = pack_f16x2(av, bv);
+                    const __half2 h2 = *reinterpret_cast<const __half2*>(&hi);
+                    ph[2 * j + x] = hi;
+                    pl[2 * j + x] = pack_f16x2(av - __low2float(h2), bv - __high2float(h2));
+                }
+            }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    o[j][0] *= al[0];
+                    o[j][1] *= al[0];
+                    o[j][2] *= al[1];
+                    o[j][3] *= al[1];
+                }
+            }
+            // ---- O += P V
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint32_t sel = (uint32_t)((j & 3) | ((4 + (j & 3)) << 4));
+                const uint32_t b0 = codes_to_f16x2(__byte_perm(vv[0][j >> 2], vv[1][j >> 2], sel));
+                const uint32_t b1 = codes_to_f16x2(__byte_perm(vv[2][j >> 2], vv[3][j >> 2], sel));
+                mma_f16(o[j], ph, b0, b1);
+                mma_f16(o[j], pl, b0, b1);
+            }
+        }
+    }
+
+    // ---- join the quads' sums, the warps, then the cluster's CTAs
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+        if (c == 0) {
+            s_m[warp][r0 + 8 * x] = m[x];
+            s_l[warp][r0 + 8 * x] = l[x];
+        }
+        const float back = m[x] == -INFINITY ? 0.f : ex2(mv[x] - m[x]);     // O into the frame of m
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            s_o[warp][r0 + 8 * x][2 * c * NT + j] = o[j][2 * x] * back;
+            s_o[warp][r0 + 8 * x][(2 * c + 1) * NT + j] = o[j][2 * x + 1] * back;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < GROUP * D; i += 32 * GROUP_WARPS) {
+        const int r = i / D, d = i - r * D;
+        float mc = -INFINITY, lc = 0.f, oc = 0.f;
+#pragma unroll
+        for (int w = 0; w < GROUP_WARPS; ++w) mc = fmaxf(mc, s_m[w][r]);
+#pragma unroll
+        for (int w = 0; w < GROUP_WARPS; ++w) {
+            const float a = s_m[w][r] == -INFINITY ? 0.f : ex2(s_m[w][r] - mc);
+            lc += s_l[w][r] * a;
+            oc += s_o[w][r][d] * a;
+        }
+        s_o[0][r][d] = oc;                                   // read by this thread alone until here
+        if (d == 0) {
+            s_ml[r][0] = mc;
+            s_ml[r][1] = lc;
+        }
+    }
+    cg::cluster_group cluster = cg::this_cluster();
+    if (csize > 1) cluster.sync();
+    else __syncthreads();
+    // each CTA of the cluster writes its share of the rows
+    for (int r = rank; r < GROUP; r += csize) {
+        if (s_t[r] < 0) continue;                            // an unused place: its row stays as it was
+        const size_t row = (size_t)g * n + first + r;
+        for (int d = tid; d < D; d += 32 * GROUP_WARPS) {
+            float mc = -INFINITY, lc = 0.f, oc = 0.f;
+            for (int k = 0; k < csize; ++k) {
+                const float* ml = csize > 1 ? cluster.map_shared_rank(&s_ml[r][0], k) : &s_ml[r][0];
+                const float* os = csize > 1 ? cluster.map_shared_rank(&s_o[0][r][0], k) : &s_o[0][r][0];
+                const float mo = ml[0];
+                if (mo == -INFINITY) continue;
+                const float mn = fmaxf(mc, mo), a = ex2(mc - mn), b = ex2(mo - mn);
+                lc = lc * a + ml[1] * b;
+                oc = oc * a + os[d] * b;
+                mc = mn;
+            }
+            const float val = lc > 0.f ? oc / lc : 0.f;
+            if (out_bf16) static_cast<__nv_bfloat16*>(out)[row * D + d] = __float2bfloat16(val);
+            else static_cast<float*>(out)[row * D + d] = val;
+            if (d == 0) lse[row] = lc > 0.f ? (mc + log2f(lc)) * 0.69314718055994531f : -INFINITY;
+        }
     }
     if (csize > 1) cluster.sync();                           // the others' shared memory stays until it has been read
 }

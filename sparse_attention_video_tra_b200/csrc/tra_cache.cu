@@ -124,15 +124,26 @@ extern "C" tra_status tra_cache_attention_tokens(tra_plan plan, const void* q, c
     if (cache_bytes < cache_layout(G).cache_bytes) return TRA_ERR_WORKSPACE;
     const long long units = (long long)n * G.G;
     if (units > (1ll << 31) - 1) return TRA_ERR_UNSUPPORTED;
-    // CTAs per token and head: as many as keep all of them resident at once
+    // Groups of 16 tokens share a key's codes on the tensor cores once that fills
+    // the card; below, one token at a time over more CTAs.  Measured cold, one
+    // token at a time / grouped: 45 / 53 us for 1 token and 40 heads at
+    // 21 x 45 x 80, 121 / 64 for 2 and 338 / 86 for 16; 39 / 28 for 6 tokens and
+    // 12 heads at 21 x 30 x 52, but 27 / 23 for 4 and 12 / 16 for 8 tokens and 4
+    // heads at 9 x 17 x 23.
+    const bool grouped = n >= 2 && units >= 64;
+    const long long work = grouped ? (long long)((n + tra::GROUP - 1) / tra::GROUP) * G.G : units;
+    // CTAs per group or token and head, a cluster: as many as stay resident
+    // together; 16 (35 -> 26 us for 1 token and 12 heads) while they cost no
+    // other its place
     int csize = 8;
-    while (csize > 1 && units * csize > 148 * 4) csize /= 2;
-    if (units * csize > (1ll << 31) - 1) return TRA_ERR_UNSUPPORTED;
+    while (csize > 1 && work * csize > 148 * (grouped ? 2 : 4)) csize /= 2;
+    if (!grouped && work * 16 <= 148 * 2) csize = 16;
+    if (work * csize > (1ll << 31) - 1) return TRA_ERR_UNSUPPORTED;
 
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
-    cfg.gridDim = dim3((unsigned)(units * csize));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)(work * csize));
+    cfg.blockDim = dim3(grouped ? 32 * tra::GROUP_WARPS : 256);
     cfg.stream = (cudaStream_t)stream;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = (unsigned)csize;
@@ -140,11 +151,19 @@ extern "C" tra_status tra_cache_attention_tokens(tra_plan plan, const void* q, c
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     const int bf16 = (plan->flags & TRA_FLAG_OUT_BF16) != 0 ? 1 : 0;
-    auto go = [&](auto kern) {
-        return cudaLaunchKernelEx(&cfg, kern, G, cache_view(G, cache), (const uint4*)q, token, radius, n, cached_frames, csize,
-                                  out, bf16, lse) == cudaSuccess;
+    cfg.dynamicSmemBytes = !grouped ? 0 : G.D == 64 ? tra::group_smem_bytes<64>() : tra::group_smem_bytes<128>();
+    auto go = [&](auto one, auto many) {
+        if (grouped && !set_smem(many, (int)cfg.dynamicSmemBytes)) return false;
+        if (csize > 8 && cudaFuncSetAttribute(one, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
+        return (grouped ? cudaLaunchKernelEx(&cfg, many, G, cache_view(G, cache), (const uint32_t*)q, token, radius, n,
+                                             cached_frames, csize, out, bf16, lse)
+                        : cudaLaunchKernelEx(&cfg, one, G, cache_view(G, cache), (const uint4*)q, token, radius, n,
+                                             cached_frames, csize, out, bf16, lse)) == cudaSuccess;
     };
-    const bool ok = G.D == 64 ? (G.disk ? go(tra::token_attention_kernel<64, true>) : go(tra::token_attention_kernel<64, false>))
-                              : (G.disk ? go(tra::token_attention_kernel<128, true>) : go(tra::token_attention_kernel<128, false>));
+    bool ok;
+    if (G.D == 64) ok = G.disk ? go(tra::token_attention_kernel<64, true>, tra::token_group_kernel<64, true>)
+                               : go(tra::token_attention_kernel<64, false>, tra::token_group_kernel<64, false>);
+    else ok = G.disk ? go(tra::token_attention_kernel<128, true>, tra::token_group_kernel<128, true>)
+                     : go(tra::token_attention_kernel<128, false>, tra::token_group_kernel<128, false>);
     return ok ? launch_status() : TRA_ERR_CUDA;
 }

@@ -215,7 +215,7 @@ def test_tokens_over_the_cache(grid, flags):
     s = Setup(*grid, flags)
     T, H, W = s.grid
     g = torch.Generator(device="cuda").manual_seed(2)
-    for n, cached in ((1, T), (3, max(0, T - 1)), (17, T), (2, 0)):
+    for n, cached in ((1, T), (3, max(0, T - 1)), (17, T), (2, 0), (97, T), (83, max(0, T - 1)), (70, 0)):
         s.cache.fill_(0x7F)
         if cached:
             s.store(0, cached)
@@ -233,6 +233,26 @@ def test_tokens_over_the_cache(grid, flags):
         ref.check(lse, l, le, "lse")
         empty = ~keep.any(-1)
         assert not out[empty].any() and torch.isneginf(lse[empty]).all()
+
+
+@pytest.mark.parametrize("n", [5, 100])
+@pytest.mark.parametrize("d", [64, 128])
+def test_tokens_over_tiles_of_very_different_scales(n, d):
+    """Values of frames that differ by up to 2^40, keys that reach scores of +-100, query rows from 2^-30 to 2^7."""
+    s = Setup(6, 12, 11, 2, d, 0.9, 2, N_)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    frame = torch.arange(s.i.N, device="cuda") // (12 * 11)
+    s.v.mul_(torch.exp2(torch.tensor([0.0, 20.0, -20.0, 3.0, -20.0, 20.0], device="cuda"))[frame][None, :, None].bfloat16())
+    s.q.mul_(torch.exp2(torch.randint(-30, 8, (2, s.i.N, 1), generator=g, device="cuda").float()).bfloat16())
+    s.store()
+    token = torch.randint(0, s.i.N, (n,), generator=g, device="cuda", dtype=torch.int32)
+    radius = torch.randint(0, 8, (2, n), generator=g, device="cuda", dtype=torch.int32)
+    out, lse = s.tokens(token, radius, 6)
+    s.ok()
+    keep = ref.pairs_kept(6, 12, 11, 0.9, 2, token.long(), torch.arange(s.i.N, device="cuda"), radius)
+    o, l, oe, le = ref.attention(s.q[:, token.long()], *s.held(), keep, 2.0 ** -20)
+    ref.check(out, o, oe, "out")
+    ref.check(lse, l, le, "lse")
 
 
 def test_many_tokens_and_unused_places():
