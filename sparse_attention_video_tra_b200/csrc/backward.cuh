@@ -5,19 +5,19 @@
 //     dS_ij = P_ij (dP_ij - D_i)
 //     dV_j = sum_i P_ij dO_i,  dK_j = sum_i dS_ij q_i / sqrt d,
 //     dQ_i = sum_j dS_ij k_j / sqrt d.
-// Four launches after a memset of the tile bitmaps:
+// Three launches:
 //   backward_rows   D_i, the log2-domain lse and the grid position of every
-//                   query row in mask-slot order, and the operands copied to
-//                   plain rows where the caller's are not
+//                   query row in mask-slot order, the operands copied to
+//                   plain rows where the caller's are not, the tile bitmaps cleared
 //   transpose_lists the mask's key-tile lists as bits per (key tile, query slot)
-//   backward_kv     one CTA per key tile: dK and dV over the query slots that
-//                   list it
-//   backward_q      one CTA per query slot: dQ over its key tiles
-// S and dP are computed in both of the last two (7 products per tile pair where
+//   backward        one CTA per key tile: dK and dV over the query slots that
+//                   list it (backward_kv); and one CTA per query slot: dQ over
+//                   its key tiles (backward_q)
+// S and dP are computed in both parts of the last (7 products per tile pair where
 // 5 would do with dQ added up across CTAs): every output row is then written
 // once, by one CTA, with a fixed order of summation, so the gradients are
 // bit-identical from run to run, no fp32 dQ buffer is needed, and neither
-// kernel moves P or dS through shared memory: each keeps the rows it sums over
+// part moves P or dS through shared memory: each keeps the rows it sums over
 // in the tensor memory's columns and the rows it owns in its lanes.
 // P and dS are rounded to bf16 for the tensor cores (at most 2^-8 of each
 // value, as P in the forward pass); all sums are fp32.
@@ -30,7 +30,7 @@
 
 namespace tra {
 
-// What the two gradient kernels read besides the tensor maps.
+// What the gradient kernel reads besides the tensor maps.
 struct BwdArgs {
     const uint8_t* mask;
     const float4* rows;          // [heads][nQ][128] slot order: lse * log2 e, D_i, h | w << 8 (bits), radius (bits)
@@ -74,7 +74,8 @@ template <int D, bool IN_F32>
 __global__ void __launch_bounds__(256)
 backward_rows_kernel(const Geom G, const uint8_t* __restrict__ mask, const void* __restrict__ out,
                      const void* __restrict__ dout, const float* __restrict__ lse, const uint4* __restrict__ q,
-                     const uint4* __restrict__ k, const uint4* __restrict__ v, float4* __restrict__ rows, const RowCopies copy)
+                     const uint4* __restrict__ k, const uint4* __restrict__ v, float4* __restrict__ rows, const RowCopies copy,
+                     uint32_t* __restrict__ bits, int bw)
 {
     constexpr int LPR = D / 8;                                        // lanes per row
     const int g = blockIdx.y, sub = threadIdx.x % LPR;
@@ -90,6 +91,8 @@ backward_rows_kernel(const Geom G, const uint8_t* __restrict__ mask, const void*
         trow = ((t * G.nTh + tr) * G.nTw + tc) * 128 + i;
         return h < G.H && w < G.W;
     };
+    // the head's tile bitmaps, nQ * bw words, over its blocks
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < G.nQ * bw; i += gridDim.x * 256) bits[(size_t)g * G.nQ * bw + i] = 0u;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     int h, w, trow;
     if (copy.k) {
@@ -280,7 +283,6 @@ struct BwdKvCfg {
     static constexpr int OFF_ZERO = OFF_META + MST * META;  // a plane of zeros
     static constexpr int OFF_BARS = OFF_ZERO + 2048;
     static constexpr int OFF_LIST = OFF_BARS + 40 * 8 + 64; // uint16 [list_cap]
-    static constexpr int THREADS = 384;
     static constexpr int REGS_SOFTMAX = 216, REGS_OTHER = 72;
     static int smem(int list_cap) { return OFF_LIST + ((list_cap * 2 + 15) & ~15) + 1024; }
     // The ring tiles of slot j's Q and dO.  dO of a slot is done with half a step
@@ -292,15 +294,11 @@ struct BwdKvCfg {
 };
 
 template <int D, int TWL, bool DISK>
-__global__ void __launch_bounds__(384, 1)
-backward_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, const Geom G,
-                   const BwdArgs A)
+__device__ __forceinline__ void backward_kv(uint8_t* smem, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                            const CUtensorMap& tm_do, const Geom& G, const BwdArgs& A)
 {
     using C = BwdKvCfg<D>;
     constexpr int TW = 1 << TWL;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
     uint64_t* kv_full = bars;
     uint64_t* r_full = bars + 1;                 // [4]: ring tiles
@@ -689,21 +687,16 @@ struct BwdQCfg {
     static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + KST * TILE;
     static constexpr int OFF_BARS = OFF_V + VST * TILE;
     static constexpr int BYTES = OFF_BARS + 24 * 8 + 32;
-    static constexpr int THREADS = 384;
     static constexpr int REGS_SOFTMAX = 216, REGS_OTHER = 72;
     static int smem() { return BYTES + 1024; }
 };
 
 template <int D, int TWL, bool DISK>
-__global__ void __launch_bounds__(384, 1)
-backward_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, const Geom G,
-                  const BwdArgs A)
+__device__ __forceinline__ void backward_q(uint8_t* smem, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                           const CUtensorMap& tm_do, const Geom& G, const BwdArgs& A)
 {
     using C = BwdQCfg<D>;
     constexpr int TW = 1 << TWL;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
     uint64_t* q_full = bars;
     uint64_t* k_full = bars + 1;                 // [KST]
@@ -974,6 +967,21 @@ backward_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// Both in one launch, the longer key tiles (z = 0) first: neither needs the other,
+// a small grid fills the SMs with both at once (5 x 17 x 23, 3 heads: 75 CTAs
+// each), and the query slots fill the tail of the key tiles.
+template <int D, int TWL, bool DISK>
+__global__ void __launch_bounds__(384, 1)
+backward_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                const __grid_constant__ Geom G, const __grid_constant__ BwdArgs A)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    if (blockIdx.z == 0) backward_kv<D, TWL, DISK>(smem, tm_q, tm_k, tm_v, tm_do, G, A);
+    else backward_q<D, TWL, DISK>(smem, tm_q, tm_k, tm_v, tm_do, G, A);
 }
 
 }  // namespace tra

@@ -29,7 +29,7 @@ namespace {
 struct BwdLayout {
     bool copy_q, copy_kv;                    // dO always has its copy
     int bw;
-    size_t off_bits, bits_bytes, off_do, off_q, off_k, off_v, total;
+    size_t off_bits, off_do, off_q, off_k, off_v, total;
 };
 
 BwdLayout backward_layout(tra_plan plan)
@@ -42,8 +42,7 @@ BwdLayout backward_layout(tra_plan plan)
     const size_t rows = (size_t)G.G * G.N_pad, tile_rows = rows * G.D * 2;
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     L.off_bits = up(rows * sizeof(float4));
-    L.bits_bytes = (size_t)G.G * G.nQ * L.bw * 4;
-    L.off_do = up(L.off_bits + L.bits_bytes);
+    L.off_do = up(L.off_bits + (size_t)G.G * G.nQ * L.bw * 4);
     L.off_q = up(L.off_do + tile_rows);
     L.off_k = up(L.off_q + (L.copy_q ? tile_rows : 0));
     L.off_v = up(L.off_k + (L.copy_kv ? tile_rows : 0));
@@ -55,15 +54,11 @@ template <int D, int TWL, bool DISK>
 tra_status run_backward(const tra::Geom& G, const tra::BwdArgs& A, const CUtensorMap& q, const CUtensorMap& k,
                         const CUtensorMap& v, const CUtensorMap& d, cudaStream_t st)
 {
-    using KV = tra::BwdKvCfg<D>;
-    using Q = tra::BwdQCfg<D>;
-    auto kv = tra::backward_kv_kernel<D, TWL, DISK>;
-    auto qk = tra::backward_q_kernel<D, TWL, DISK>;
-    const int smem_kv = KV::smem(G.list_cap), smem_q = Q::smem();
-    if (smem_kv > kMaxSmem || smem_q > kMaxSmem) return TRA_ERR_UNSUPPORTED;
-    if (!set_smem(kv, smem_kv) || !set_smem(qk, smem_q)) return TRA_ERR_CUDA;
-    kv<<<dim3(G.nQ, G.G), KV::THREADS, smem_kv, st>>>(q, k, v, d, G, A);
-    qk<<<dim3(G.nQ, G.G), Q::THREADS, smem_q, st>>>(q, k, v, d, G, A);
+    auto kern = tra::backward_kernel<D, TWL, DISK>;
+    const int smem = std::max(tra::BwdKvCfg<D>::smem(G.list_cap), tra::BwdQCfg<D>::smem());
+    if (smem > kMaxSmem) return TRA_ERR_UNSUPPORTED;
+    if (!set_smem(kern, smem)) return TRA_ERR_CUDA;
+    kern<<<dim3(G.nQ, G.G, 2), 384, smem, st>>>(q, k, v, d, G, A);
     return launch_status();
 }
 
@@ -115,10 +110,10 @@ extern "C" tra_status tra_attention_backward(tra_plan plan, const void* q, const
     A.dq = dq; A.dk = dk; A.dv = dv;
     A.grad_scale = (float)(1.0 / std::sqrt((double)G.D));
 
-    if (cudaMemsetAsync(ws + L.off_bits, 0, L.bits_bytes, st) != cudaSuccess) return TRA_ERR_CUDA;
     const dim3 row_grid(G.N_pad * (G.D / 8) / 256, G.G);
     auto go = [&](auto kern) {
-        kern<<<row_grid, 256, 0, st>>>(G, A.mask, out, dout, lse, (const uint4*)q, (const uint4*)k, (const uint4*)v, (float4*)ws, copy);
+        kern<<<row_grid, 256, 0, st>>>(G, A.mask, out, dout, lse, (const uint4*)q, (const uint4*)k, (const uint4*)v, (float4*)ws, copy,
+                                         (uint32_t*)(ws + L.off_bits), L.bw);
     };
     if (G.D == 64) bf16 ? go(tra::backward_rows_kernel<64, false>) : go(tra::backward_rows_kernel<64, true>);
     else bf16 ? go(tra::backward_rows_kernel<128, false>) : go(tra::backward_rows_kernel<128, true>);
