@@ -110,6 +110,7 @@ constexpr uint32_t MT_IN0 = 1u << 26, MT_FULL0 = 1u << 28;
 // of the key frames [k0, k1) only.
 struct Span {
     int q0, nq, k0, k1;
+    int lone;                    // LSE: one query tile (slot) per CTA
 };
 
 // LSE: also write each row's log-sum-exp (natural log) to `lse`; O is then
@@ -170,7 +171,14 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         qa = (q0 + nq - 1) * tpf + 2 * (pair - paired);
         qb = qa + 1;
     }
-    const bool hasB = qb < (q0 + nq) * tpf;
+    // a grid that leaves SMs idle takes one tile per CTA: the chain of a lone
+    // tile takes 1.4 us a key tile, that of a pair 2.5 us
+    const bool lone = LSE && span.lone;
+    if (lone) {
+        qa = q0 * tpf + pair;
+        qb = qa + 1;
+    }
+    const bool hasB = !lone && qb < (q0 + nq) * tpf;
     // the row of token (t, h, w) in q, out and lse
     auto query_row = [&](int t, int h, int w, int tile_row) -> size_t {
         if constexpr (SPAN)

@@ -19,10 +19,12 @@ tra_status run_attention(const tra::Geom& G, const CUtensorMap& q, const CUtenso
     if (!set_smem(kern, smem)) return TRA_ERR_CUDA;
     // two query tiles per CTA; with radius-sorted groups, the same slot of
     // frames 2f and 2f + 1, then an odd last frame's slots two by two
-    const int nq = SPAN ? span.nq : G.T;
-    const int ctas = G.qsort ? nq / 2 * G.tiles_per_frame + (nq % 2) * ((G.tiles_per_frame + 1) / 2)
-                             : (nq * G.tiles_per_frame + 1) / 2;
-    kern<<<dim3(ctas, G.G), C::THREADS, smem, st>>>(q, k, v, G, mask, out, qraw, lse, span);
+    const int nq = SPAN ? span.nq : G.T, tiles = nq * G.tiles_per_frame;
+    tra::Span sp = span;
+    sp.lone = LSE && (long long)tiles * G.G <= 148 ? 1 : 0;
+    const int ctas = sp.lone ? tiles
+                   : G.qsort ? nq / 2 * G.tiles_per_frame + (nq % 2) * ((G.tiles_per_frame + 1) / 2) : (tiles + 1) / 2;
+    kern<<<dim3(ctas, G.G), C::THREADS, smem, st>>>(q, k, v, G, mask, out, qraw, lse, sp);
     return launch_status();
 }
 

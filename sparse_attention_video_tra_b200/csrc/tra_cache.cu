@@ -30,7 +30,7 @@ tra::CacheView cache_view(const tra::Geom& G, const void* cache)
 // the key frames that the queries of [frame, frame + n) can reach and the cache holds
 tra::Span call_span(const tra::Geom& G, int frame, int n, int cached)
 {
-    tra::Span s = {frame, n, std::max(0, frame - G.rte), std::min(cached, std::min(G.T, frame + n + G.rte))};
+    tra::Span s = {frame, n, std::max(0, frame - G.rte), std::min(cached, std::min(G.T, frame + n + G.rte)), 0};
     if (s.k1 <= s.k0) s.k0 = s.k1 = 0;
     return s;
 }
