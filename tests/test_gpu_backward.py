@@ -207,6 +207,39 @@ def test_a_training_step_in_a_graph_and_on_another_stream():
     graph.reset()
 
 
+def test_two_backward_passes_at_once_on_two_streams():
+    """Each with its own workspace: the same bits as one after the other."""
+    sets = [Setup(5, 17, 23, 2, 128, 0.8, 3, N_ | B_, seed=x) for x in (1, 2)]
+    fwd = [s.forward() for s in sets]
+    douts = [s.dout()[1] for s in sets]
+    want = [s.backward(*f, d) for s, f, d in zip(sets, fwd, douts)]
+    torch.cuda.synchronize()
+    got = []
+    for s, f, d in zip(sets, fwd, douts):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            ws = s.plan.new_backward_workspace()
+            got.append([s.backward(*f, d, ws) for _ in range(5)])
+    torch.cuda.synchronize()
+    assert sets[0].plan.status() == 0
+    for w, g5 in zip(want, got):
+        for g in g5:
+            assert all(torch.equal(x, y) for x, y in zip(g, w))
+
+
+def test_gradients_at_a_720p_frame_grid():
+    """A grid whose key tiles are listed by hundreds of slots, against the formulas on the rows of two frames' reach."""
+    s = Setup(3, 45, 80, 1, 128, 0.8, 2, N_ | B_ | Q_, b=1.5)
+    out, lse = s.forward()
+    dout_nat, dout = s.dout()
+    grads = s.backward(out, lse, dout)
+    torch.cuda.synchronize()
+    assert s.plan.status() == 0
+    assert int(s.plan.mask_views(s.mask)[1].max()) > 60
+    want, bounds = ref.gradients(*s.nat, out, lse, dout_nat, s.keep)
+    for name, g, w, e in zip(("dq", "dk", "dv"), grads, want, bounds):
+        ref.check(g, w, e, name)
+
+
 def test_autograd_use():
     """The calls inside a torch.autograd.Function: leaf gradients are the kernels'."""
     s = Setup(3, 10, 12, 2, 64, 0.8, 1, N_)

@@ -329,6 +329,60 @@ def test_generating_a_clip_frame_by_frame(flags):
         ref.check(both, l, le + ole, "merged lse")
 
 
+def test_offsets_past_32_bits():
+    """The last heads of a cache of 4.5 GB of keys and as much of values: frames, lone tokens and grouped ones."""
+    T, H, W, heads, d = 21, 45, 80, 440, 128
+    plan = tra.Plan(T, H, W, heads, d, 1.0, -30.0, 0.8, 0, 1, N_ | B_)          # a budget of one token, no temporal reach
+    assert tra.tra_cache_query(plan.handle).off_v > 2 ** 32
+    g = torch.Generator(device="cuda").manual_seed(6)
+    k, v, q = (torch.randn(heads, H * W, d, generator=g, device="cuda").bfloat16() for _ in range(3))
+    cache = plan.new_cache()
+    plan.cache_store(k, v, 20, cache)
+    k8, v8, ks, vs = plan.cache_views(cache)
+    tpf = plan.info.n_tiles_h * plan.info.n_tiles_w
+    held = []
+    for c, s in ((k8, ks), (v8, vs)):
+        one = tra.Plan(1, H, W, 1, d, 1.0, 0.0, 0.8, 0, 1, N_)
+        held.append(gh.to_natural((c[-1:, 20 * tpf:].double() * s[-1:, 20 * tpf:].double()[..., None, None]).flatten(1, 2), one.info))
+    for n in (1, 16):
+        token = 20 * H * W + torch.randint(0, H * W, (n,), generator=g, device="cuda", dtype=torch.int32)
+        radius = torch.full((heads, n), 3, dtype=torch.int32, device="cuda")
+        qt = q[:, (token - 20 * H * W).long()].contiguous()
+        out, lse = torch.empty_like(qt), torch.empty(heads, n, device="cuda")
+        plan.cache_attention_tokens(qt, token, radius, cache, 21, out, lse)
+        keep = ref.pairs_kept(1, H, W, 0.8, 0, (token - 20 * H * W).long(), torch.arange(H * W, device="cuda"), radius[-1:])
+        o, l, oe, le = ref.attention(qt[-1:], *held, keep, 0.0)
+        ref.check(out[-1:], o, oe, "out")
+        ref.check(lse[-1:], l, le, "lse")
+    mask = plan.new_mask()
+    plan.radius_and_mask(torch.zeros(heads, T * H * W, device="cuda"), mask)
+    out, lse = torch.empty_like(q), torch.empty(heads, H * W, device="cuda")
+    plan.cache_attention(q, 20, cache, 21, mask, out, lse, plan.new_cache_workspace(1))
+    torch.cuda.synchronize()
+    assert plan.status() == 0
+    # each query keeps itself alone
+    ref.check(out[-1:], held[1], held[1].abs() * ref.BF16, "frame")
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Frames and tokens of two clips on two streams, each with its own workspace, equal the calls one after the other."""
+    a, b = (Setup(5, 17, 23, 2, 128, 0.8, 3, N_ | B_, seed=s) for s in (1, 2))
+    masks = [x.make_mask()[0] for x in (a, b)]
+    for x in (a, b):
+        x.store()
+    want = [x.frames(2, 3, 5, m) for x, m in zip((a, b), masks)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for x, m, st in zip((a, b), masks, streams):
+        with torch.cuda.stream(st):
+            got.append([x.frames(2, 3, 5, m) for _ in range(5)])
+    a.ok()
+    for w, g5 in zip(want, got):
+        for o, l in g5:
+            assert torch.equal(o, w[0]) and torch.equal(l, w[1])
+
+
 def test_graphs_and_streams():
     s = Setup(5, 17, 23, 2, 128, 0.8, 3, N_ | B_)
     mask, radius = s.make_mask()
