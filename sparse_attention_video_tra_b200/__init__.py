@@ -280,6 +280,9 @@ class Plan:
         self.flags = flags
         self.info = tra_plan_query(self.handle)
         self._cache_info = None
+        i = self.info
+        self._io_elems = i.heads * self.io_rows * i.d
+        self._frame_rows = i.H * i.W if self.natural else i.n_tiles_h * i.n_tiles_w * 128
         self.params = dict(T=T, H=H, W=W, heads=heads, d=d, a=a, b=b, gamma=gamma, Rt=Rt, Bmin=Bmin)
 
     def close(self):
@@ -419,51 +422,42 @@ class Plan:
                       self._stream(stream))
         return out
 
-    def _buffer(self, x, dtype, numel, name):
-        """A contiguous cuda tensor of `dtype` with `numel` elements (at least, for a byte buffer)."""
-        import torch
-        enough = x.numel() >= numel if dtype == torch.uint8 else x.numel() == numel
-        if x.dtype != dtype or not x.is_cuda or not x.is_contiguous() or not enough:
-            raise ValueError(f"{name}: expected contiguous cuda {dtype} with {numel} elements, "
-                             f"got {x.dtype} {tuple(x.shape)} on {x.device}")
-
-    def _on_device(self, *tensors):
-        """All tensors on one device, which has to be the current one: the launch goes to its stream."""
+    def _pointers(self, *buffers):
+        """Data pointers of (tensor, dtype, numel, name): contiguous tensors of that type and size (byte buffers: at
+        least that size) on the current device, whose stream the launch goes to.  One pass, since these checks are
+        most of a small call's time on the host."""
         import torch
         current = torch.cuda.current_device()
-        if any(x.get_device() != current for x in tensors):
-            raise ValueError(f"tensors on {sorted({str(x.device) for x in tensors})}; expected all on the current "
-                             f"device, cuda:{torch.cuda.current_device()}")
+        ptrs = []
+        for x, dtype, numel, name in buffers:
+            n = x.numel()
+            if x.dtype is not dtype or x.get_device() != current or not x.is_contiguous() or \
+                    (n < numel if dtype is torch.uint8 else n != numel):
+                raise ValueError(f"{name}: expected contiguous {dtype} with {numel} elements on the current device, "
+                                 f"cuda:{current}, got {x.dtype} {tuple(x.shape)} on {x.device}"
+                                 + ("" if x.is_contiguous() else ", not contiguous"))
+            ptrs.append(x.data_ptr())
+        return ptrs
 
     def attention_lse(self, q, k, v, mask, out, lse, stream=None):
         """tra_attention_lse: out and the rows' log-sum-exp (natural log)."""
         import torch
-        i = self.info
-        for x, nme in ((q, "q"), (k, "k"), (v, "v")):
-            self._rows(x, self.io_rows, nme)
-        self._rows(out, self.io_rows, "out", self.out_dtype)
-        self._buffer(lse, torch.float32, i.heads * self.io_rows, "lse")
-        self._buffer(mask, torch.uint8, i.mask_bytes, "mask")
-        self._on_device(q, k, v, mask, out, lse)
-        tra_attention_lse(self.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), mask.data_ptr(), out.data_ptr(),
-                          lse.data_ptr(), self._stream(stream))
+        n, bf16 = self._io_elems, torch.bfloat16
+        ptrs = self._pointers((q, bf16, n, "q"), (k, bf16, n, "k"), (v, bf16, n, "v"),
+                              (mask, torch.uint8, self.info.mask_bytes, "mask"), (out, self.out_dtype, n, "out"),
+                              (lse, torch.float32, n // self.info.d, "lse"))
+        tra_attention_lse(self.handle, *ptrs, self._stream(stream))
         return out, lse
 
     def attention_backward(self, q, k, v, mask, out, lse, dout, dq, dk, dv, workspace, stream=None):
         """tra_attention_backward: the gradients of attention_lse's out, in out's type and layout."""
         import torch
-        i = self.info
-        for x, nme in ((q, "q"), (k, "k"), (v, "v")):
-            self._rows(x, self.io_rows, nme)
-        for x, nme in ((out, "out"), (dout, "dout"), (dq, "dq"), (dk, "dk"), (dv, "dv")):
-            self._rows(x, self.io_rows, nme, self.out_dtype)
-        self._buffer(lse, torch.float32, i.heads * self.io_rows, "lse")
-        self._buffer(mask, torch.uint8, i.mask_bytes, "mask")
-        self._buffer(workspace, torch.uint8, 1, "workspace")
-        self._on_device(q, k, v, mask, out, lse, dout, dq, dk, dv, workspace)
-        tra_attention_backward(self.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), mask.data_ptr(),
-                               out.data_ptr(), lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                               dv.data_ptr(), workspace.data_ptr(), workspace.numel(), self._stream(stream))
+        n, bf16, o = self._io_elems, torch.bfloat16, self.out_dtype
+        ptrs = self._pointers((q, bf16, n, "q"), (k, bf16, n, "k"), (v, bf16, n, "v"),
+                              (mask, torch.uint8, self.info.mask_bytes, "mask"), (out, o, n, "out"),
+                              (lse, torch.float32, n // self.info.d, "lse"), (dout, o, n, "dout"), (dq, o, n, "dq"),
+                              (dk, o, n, "dk"), (dv, o, n, "dv"), (workspace, torch.uint8, 1, "workspace"))
+        tra_attention_backward(self.handle, *ptrs, workspace.numel(), self._stream(stream))
         return dq, dk, dv
 
     # -- keys and values held in 8 bits
@@ -488,7 +482,9 @@ class Plan:
         """(k codes, v codes [heads, n_tiles, 128, d] float8_e4m3fn, k scale, v scale [heads, n_tiles] fp32)."""
         import torch
         i, c = self.info, self.cache_info
-        self._buffer(cache, torch.uint8, c.cache_bytes, "cache")
+        if cache.dtype is not torch.uint8 or not cache.is_contiguous() or cache.numel() < c.cache_bytes:
+            raise ValueError(f"cache: expected contiguous uint8 with {c.cache_bytes} elements, got {cache.dtype} "
+                             f"{tuple(cache.shape)}")
         cache = cache.view(-1)[:c.cache_bytes]
         codes, scale = cache.view(torch.float8_e4m3fn), cache.view(torch.float32)
         shape, strides = (i.heads, i.n_tiles, 128, i.d), (i.N_pad * i.d, 128 * i.d, i.d, 1)
@@ -499,54 +495,41 @@ class Plan:
 
     def _frames(self, x, name) -> int:
         """How many frames of this plan's rows [heads, rows, d] x holds."""
-        i = self.info
-        per = i.H * i.W if self.natural else i.n_tiles_h * i.n_tiles_w * 128
-        if x.dim() != 3 or x.shape[0] != i.heads or x.shape[2] != i.d or x.shape[1] % per or not x.shape[1]:
-            raise ValueError(f"{name}: expected [{i.heads}, frames * {per}, {i.d}], got {tuple(x.shape)}")
-        return x.shape[1] // per
+        i, per, shape = self.info, self._frame_rows, x.shape
+        if len(shape) != 3 or shape[0] != i.heads or shape[2] != i.d or shape[1] % per or not shape[1]:
+            raise ValueError(f"{name}: expected [{i.heads}, frames * {per}, {i.d}], got {tuple(shape)}")
+        return shape[1] // per
 
     def cache_store(self, k, v, frame, cache, stream=None):
         """tra_cache_store: k and v hold the rows of the frames from `frame` on, as many as their shape says."""
         import torch
-        n = self._frames(k, "k")
-        for x, nme in ((k, "k"), (v, "v")):
-            self._rows(x, k.shape[1], nme)
-        self._buffer(cache, torch.uint8, 1, "cache")
-        self._on_device(k, v, cache)
-        tra_cache_store(self.handle, k.data_ptr(), v.data_ptr(), frame, n, cache.data_ptr(), cache.numel(),
-                        self._stream(stream))
+        frames, n = self._frames(k, "k"), k.numel()
+        ptrs = self._pointers((k, torch.bfloat16, n, "k"), (v, torch.bfloat16, n, "v"), (cache, torch.uint8, 1, "cache"))
+        tra_cache_store(self.handle, *ptrs[:2], frame, frames, ptrs[2], cache.numel(), self._stream(stream))
         return cache
 
     def cache_attention(self, q, frame, cache, cached_frames, mask, out, lse, workspace, stream=None):
         """tra_cache_attention: the queries of the frames from `frame` on, as many as q's shape says."""
         import torch
-        i = self.info
-        n = self._frames(q, "q")
-        self._rows(q, q.shape[1], "q")
-        self._rows(out, q.shape[1], "out", self.out_dtype)
-        self._buffer(lse, torch.float32, i.heads * q.shape[1], "lse")
-        self._buffer(mask, torch.uint8, i.mask_bytes, "mask")
-        self._buffer(cache, torch.uint8, 1, "cache")
-        self._buffer(workspace, torch.uint8, 1, "workspace")
-        self._on_device(q, cache, mask, out, lse, workspace)
-        tra_cache_attention(self.handle, q.data_ptr(), frame, n, cache.data_ptr(), cache.numel(), cached_frames,
-                            mask.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                            self._stream(stream))
+        frames, n = self._frames(q, "q"), q.numel()
+        qp, cp, mp, op, lp, wp = self._pointers(
+            (q, torch.bfloat16, n, "q"), (cache, torch.uint8, 1, "cache"),
+            (mask, torch.uint8, self.info.mask_bytes, "mask"), (out, self.out_dtype, n, "out"),
+            (lse, torch.float32, n // self.info.d, "lse"), (workspace, torch.uint8, 1, "workspace"))
+        tra_cache_attention(self.handle, qp, frame, frames, cp, cache.numel(), cached_frames, mp, op, lp, wp,
+                            workspace.numel(), self._stream(stream))
         return out, lse
 
     def cache_attention_tokens(self, q, token, radius, cache, cached_frames, out, lse, stream=None):
         """tra_cache_attention_tokens: q [heads, n, d], token int32 [n], radius int32 [heads, n]."""
         import torch
-        i, n = self.info, token.numel()
-        self._rows(q, n, "q")
-        self._rows(out, n, "out", self.out_dtype)
-        self._buffer(token, torch.int32, n, "token")
-        self._buffer(radius, torch.int32, i.heads * n, "radius")
-        self._buffer(lse, torch.float32, i.heads * n, "lse")
-        self._buffer(cache, torch.uint8, 1, "cache")
-        self._on_device(q, token, radius, cache, out, lse)
-        tra_cache_attention_tokens(self.handle, q.data_ptr(), token.data_ptr(), radius.data_ptr(), n, cache.data_ptr(),
-                                   cache.numel(), cached_frames, out.data_ptr(), lse.data_ptr(), self._stream(stream))
+        n, rows = token.numel(), self.info.heads * token.numel()
+        qp, tp, rp, cp, op, lp = self._pointers(
+            (q, torch.bfloat16, rows * self.info.d, "q"), (token, torch.int32, n, "token"),
+            (radius, torch.int32, rows, "radius"), (cache, torch.uint8, 1, "cache"),
+            (out, self.out_dtype, rows * self.info.d, "out"), (lse, torch.float32, rows, "lse"))
+        tra_cache_attention_tokens(self.handle, qp, tp, rp, n, cp, cache.numel(), cached_frames, op, lp,
+                                   self._stream(stream))
         return out, lse
 
     def calibrate_topk(self, q, k, mass, query_tile_stride=1, stream=None):

@@ -13,10 +13,10 @@ tra_status run_attention(const tra::Geom& G, const CUtensorMap& q, const CUtenso
                          const tra::Span& span, cudaStream_t st)
 {
     using C = tra::AttnCfg<D>;
-    auto kern = tra::attention_kernel<D, TWL, OB, DISK, LSE, SPAN>;
+    constexpr auto kern = tra::attention_kernel<D, TWL, OB, DISK, LSE, SPAN>;
     const int smem = tra::attn_smem_bytes<D>(G.list_cap, G.rte, G.tiles_per_frame);
     if (smem > kMaxSmem) return TRA_ERR_UNSUPPORTED;
-    if (!set_smem(kern, smem)) return TRA_ERR_CUDA;
+    if (!allow_max_smem<kern>()) return TRA_ERR_CUDA;
     // two query tiles per CTA; with radius-sorted groups, the same slot of
     // frames 2f and 2f + 1, then an odd last frame's slots two by two
     const int nq = SPAN ? span.nq : G.T, tiles = nq * G.tiles_per_frame;

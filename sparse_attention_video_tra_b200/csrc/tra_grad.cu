@@ -54,10 +54,10 @@ template <int D, int TWL, bool DISK>
 tra_status run_backward(const tra::Geom& G, const tra::BwdArgs& A, const CUtensorMap& q, const CUtensorMap& k,
                         const CUtensorMap& v, const CUtensorMap& d, cudaStream_t st)
 {
-    auto kern = tra::backward_kernel<D, TWL, DISK>;
+    constexpr auto kern = tra::backward_kernel<D, TWL, DISK>;
     const int smem = std::max(tra::BwdKvCfg<D>::smem(G.list_cap), tra::BwdQCfg<D>::smem());
     if (smem > kMaxSmem) return TRA_ERR_UNSUPPORTED;
-    if (!set_smem(kern, smem)) return TRA_ERR_CUDA;
+    if (!allow_max_smem<kern>()) return TRA_ERR_CUDA;
     kern<<<dim3(G.nQ, G.G, 2), 384, smem, st>>>(q, k, v, d, G, A);
     return launch_status();
 }

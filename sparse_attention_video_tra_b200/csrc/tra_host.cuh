@@ -3,6 +3,7 @@
 // translation unit that includes it.
 #pragma once
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -96,6 +97,22 @@ bool take_error_word(unsigned int& word)
         if (cudaMemcpyToSymbol(tra::g_tra_error, &zero, sizeof zero) != cudaSuccess) return false;
     }
     word |= w;
+    return true;
+}
+
+// Lets KERNEL (no static shared memory) use all of a CTA's shared memory, once
+// per device: the attribute outlives the call, and setting it costs about as
+// much as a launch.
+template <auto KERNEL>
+bool allow_max_smem()
+{
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (!set_smem(KERNEL, kMaxSmem)) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
     return true;
 }
 
