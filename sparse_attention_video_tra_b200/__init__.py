@@ -299,7 +299,11 @@ class Plan:
     # -- buffers
     def _stream(self, stream):
         import torch
-        return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+        if stream is not None:
+            return stream.cuda_stream
+        # the handle alone, where this torch gives it: a Stream object takes 3 us
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
 
     def _rows(self, x, rows, name, dtype=None):
         import torch
