@@ -573,7 +573,8 @@ token_group_kernel(const Geom G, const CacheView C, const uint32_t* __restrict__
                     const int lo = F.y0 * row_granules + F.x0;
                     end = F.y1 * row_granules + F.x1;
                     // numbers of this warp are wid + 29 frame (an odd step) modulo the warps
-                    at = lo + ((wid + 29 * (fb + f) - lo) & (warps - 1));
+                    const int off = (wid + 29 * (fb + f) - lo) % warps;
+                    at = lo + (off < 0 ? off + warps : off);
                 }
                 const int gy = (int)(((float)at + 0.5f) * inv_row), gx = at - gy * row_granules;    // at < 2^16: exact
                 at += warps;

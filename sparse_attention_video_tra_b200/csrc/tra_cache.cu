@@ -132,12 +132,18 @@ extern "C" tra_status tra_cache_attention_tokens(tra_plan plan, const void* q, c
     // heads at 9 x 17 x 23.
     const bool grouped = n >= 2 && units >= 64;
     const long long work = grouped ? (long long)((n + tra::GROUP - 1) / tra::GROUP) * G.G : units;
-    // CTAs per group or token and head, a cluster: as many as stay resident
-    // together; 16 (35 -> 26 us for 1 token and 12 heads) while they cost no
-    // other its place
+    // CTAs per group or token and head, a cluster.  Groups run one CTA per SM: the
+    // most that all run at once, counting that a cluster lies within one GPC and
+    // large ones leave SMs over (24 clusters of 5: 41 us, of 6: 59 us; 48 of
+    // 3: 65 us, of 4: 72 us).  Lone tokens: as many as stay resident together, 16
+    // (35 -> 26 us for 1 token and 12 heads) while they cost no other its place.
     int csize = 8;
-    while (csize > 1 && work * csize > 148 * (grouped ? 2 : 4)) csize /= 2;
-    if (!grouped && work * 16 <= 148 * 2) csize = 16;
+    if (grouped) {
+        while (csize > 2 && work * csize > (csize > 4 ? 128 : 144)) --csize;
+    } else {
+        while (csize > 1 && work * csize > 148 * 4) csize /= 2;
+        if (work * 16 <= 148 * 2) csize = 16;
+    }
     if (work * csize > (1ll << 31) - 1) return TRA_ERR_UNSUPPORTED;
 
     cudaLaunchConfig_t cfg = {};
