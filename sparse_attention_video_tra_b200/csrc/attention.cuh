@@ -110,7 +110,7 @@ constexpr uint32_t MT_IN0 = 1u << 26, MT_FULL0 = 1u << 28;
 // of the key frames [k0, k1) only.
 struct Span {
     int q0, nq, k0, k1;
-    int lone;                    // LSE: one query tile (slot) per CTA
+    int parts;                   // LONE: CTAs of the cluster that shares a tile's keys
 };
 
 // LSE: also write each row's log-sum-exp (natural log) to `lse`; O is then
@@ -118,7 +118,12 @@ struct Span {
 // SPAN (with LSE): the queries of some frames over the keys of some frames;
 // listed key tiles outside them are passed over, and a row that is left with
 // no key gets zeros and -inf.
-template <int D, int TWL, bool OUT_BF16, bool DISK, bool LSE, bool SPAN>
+// LONE (with LSE), for grids that leave SMs idle: one query tile (slot) per CTA,
+// or per cluster of two or four CTAs that take a part of its key tiles each and
+// join their O, maxima and sums through distributed shared memory.  The chain
+// of a lone tile takes 1.9 us a key tile, that of a pair 2.5 us; 3 frames of
+// 17 x 23 over 6, 4 heads: 78 us in pairs, 60 us alone, 39 us in clusters of two.
+template <int D, int TWL, bool OUT_BF16, bool DISK, bool LSE, bool SPAN, bool LONE>
 __global__ void __launch_bounds__(384, 1)
 attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const Geom G, const uint8_t* __restrict__ mask,
@@ -171,14 +176,12 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         qa = (q0 + nq - 1) * tpf + 2 * (pair - paired);
         qb = qa + 1;
     }
-    // a grid that leaves SMs idle takes one tile per CTA: the chain of a lone
-    // tile takes 1.4 us a key tile, that of a pair 2.5 us
-    const bool lone = LSE && span.lone;
-    if (lone) {
-        qa = q0 * tpf + pair;
+    const int parts = LONE ? span.parts : 1, part = LONE ? pair % parts : 0;
+    if (LONE) {
+        qa = q0 * tpf + pair / parts;
         qb = qa + 1;
     }
-    const bool hasB = !lone && qb < (q0 + nq) * tpf;
+    const bool hasB = !LONE && qb < (q0 + nq) * tpf;
     // the row of token (t, h, w) in q, out and lse
     auto query_row = [&](int t, int h, int w, int tile_row) -> size_t {
         if constexpr (SPAN)
@@ -338,7 +341,12 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    const int n = *s_n;
+    int n = *s_n;
+    if (LONE && parts > 1) {                                // this CTA's part of the list
+        const int lo = n * part / parts;
+        n = n * (part + 1) / parts - lo;
+        merged += lo;
+    }
     uint8_t* sQ = smem + C::OFF_Q;
     uint8_t* sK = smem + C::OFF_K;
     uint8_t* sV = smem + C::OFF_V;
@@ -552,6 +560,11 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_wait(&drain[w], 0, G.drain_ns);
         }
       }
+      if (LONE && parts > 1) {
+          __syncwarp();
+          cluster_sync();
+          cluster_sync();
+      }
     } else {
         regs_inc<C::REGS_SOFTMAX>();
         // ------------------------------------------------ softmax / epilogue (warps 0-7)
@@ -731,7 +744,71 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_arrive(&p_full[w]);
             ++k;
         }
-        if (ok && (k > 0 || (SPAN && active))) {
+        if (LONE && parts > 1) {
+            if (ok && k > 0) ok = role_wait(&pv_done[w], (k - 1) & 1, G.wait_ns, s_abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (active) {
+                // unnormalised O, its maximum and sum into this CTA's shared memory (Q, K
+                // and V are done with); 16-byte chunks of a row swizzled over the banks
+                tc_fence_after();
+                __syncwarp();
+                float4* po = reinterpret_cast<float4*>(smem) + row * (D / 4);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    if (ok && k > 0) {
+                        tmem_ld32(tmem + lane_base + colO + c * 32, v);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        po[(c * 8 + i) ^ (row & 7)] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                                  __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                }
+                reinterpret_cast<float2*>(smem + 128 * D * 4)[row] = make_float2(m_run, ok && k > 0 ? l : 0.f);
+            }
+            cluster_sync();
+            // each CTA joins its share of the rows: 8 warps, a thread per 16-byte chunk
+            const int rows = 128 / parts;
+            for (int e = tid; e < rows * (D / 4); e += 256) {
+                const int r = part * rows + e / (D / 4), ch = e % (D / 4);
+                float mj = -INFINITY, lj = 0.f;
+                float4 oj = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int p = 0; p < parts; ++p) {
+                    const float2 ml = cluster_load_f2(smem + 128 * D * 4 + r * 8, p);
+                    if (ml.y == 0.f) continue;              // this part kept no key
+                    const float4 o = cluster_load_f4(smem + (r * (D / 4) + (ch ^ (r & 7))) * 16, p);
+                    const float mn = fmaxf(mj, ml.x), a = ex2(mj - mn), b = ex2(ml.x - mn);
+                    lj = lj * a + ml.y * b;
+                    oj = make_float4(oj.x * a + o.x * b, oj.y * a + o.y * b, oj.z * a + o.z * b, oj.w * a + o.w * b);
+                    mj = mn;
+                }
+                int t, tr, tc, i = r;
+                tile_coords(G, qa, t, tr, tc);
+                bool named = true;
+                if (G.qsort) {
+                    const int l0 = grp_a[r];
+                    named = l0 < 128 * G.nTh;
+                    tr = l0 >> 7;
+                    i = l0 & 127;
+                }
+                const int h = tr * G.th + (i >> TWL), w_ = tc * TW + (i & (TW - 1));
+                if (!named || (G.natural && !(h < G.H && w_ < G.W))) continue;
+                const size_t orow = query_row(t, h, w_, ((t * G.nTh + tr) * G.nTw + tc) * 128 + i);
+                const float inv = lj > 0.f ? 1.f / lj : 0.f;
+                if constexpr (OUT_BF16)
+                    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + orow * D)[ch] =
+                        make_uint2(pack_bf16x2(oj.x * inv, oj.y * inv), pack_bf16x2(oj.z * inv, oj.w * inv));
+                else
+                    reinterpret_cast<float4*>(static_cast<float*>(out) + orow * D)[ch] =
+                        make_float4(oj.x * inv, oj.y * inv, oj.z * inv, oj.w * inv);
+                if (ch == 0) lse[orow] = lj > 0.f ? (mj + log2f(lj)) * 0.69314718055994531f : -INFINITY;
+            }
+            cluster_sync();                                 // the others' shared memory stays until it has been read
+        } else if (ok && (k > 0 || (SPAN && active))) {
             ok = k == 0 || role_wait(&pv_done[w], (k - 1) & 1, G.wait_ns, s_abort);
             if (__all_sync(0xffffffffu, ok)) {
                 tc_fence_after();

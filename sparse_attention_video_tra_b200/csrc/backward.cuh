@@ -976,8 +976,8 @@ __device__ __forceinline__ void backward_q(uint8_t* smem, const CUtensorMap& tm_
 // Tensor-bound on the tiles it computes: at 21 x 45 x 80, 4 heads, d = 128, sorted
 // groups, 462 241 tile pairs of 7 products take 10.3 ms, 1.32 PFLOP/s (0.94 of
 // what a plain bf16 product sustains on this card); one part alone takes 3280
-// (dK, dV: 2176 of products) and 2390 cycles a pair (dQ: 1536).  Of a pair's
-// elements 43 % are kept there, so the rate over kept pairs is 0.30 PFLOP/s of
+// (dK, dV: 2176 of products) and 2390 cycles a pair (dQ: 1536).  A third of a
+// pair's elements are kept there, so the rate over kept pairs is 0.30 PFLOP/s of
 // the 5 products that the gradients need.
 template <int D, int TWL, bool DISK>
 __global__ void __launch_bounds__(384, 1)

@@ -84,6 +84,9 @@ bool set_smem(K kernel, int bytes)
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
 }
 
+// streaming multiprocessors of the card
+constexpr int kSMs = 148;
+
 // largest dynamic shared memory a CTA may use on sm_100
 constexpr int kMaxSmem = 232448;
 

@@ -84,6 +84,11 @@ CASES = [
     (7, 1, 5, 3, 64, 0.8, 2, N_),
     (9, 24, 10, 2, 128, 0.8, 0, N_ | B_),               # no temporal reach
     (9, 24, 10, 1, 128, 1.0, 8, N_ | B_),               # every frame reaches every frame
+    # more query tiles than SMs: two tiles per CTA
+    (5, 17, 23, 8, 64, 0.8, 3, N_ | B_),
+    (5, 17, 23, 8, 128, 0.8, 3, 0),
+    (5, 17, 23, 8, 128, 0.8, 3, Q_ | N_ | tra.tra_flag_tile_w(8)),
+    (5, 17, 23, 8, 64, 0.8, 3, Q_ | D_ | B_ | tra.tra_flag_tile_w(8)),
 ]
 
 

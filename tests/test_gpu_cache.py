@@ -186,6 +186,12 @@ FRAME_CASES = [
     ((7, 12, 11, 3, 64, 0.8, 2), 0, 5, 2, 4),            # likewise, with pad rows
     ((7, 12, 11, 3, 64, 0.8, 2), N_ | B_, 1, 2, 0),      # nothing is cached
     ((7, 12, 11, 3, 64, 0.8, 2), 0, 6, 1, 2),            # nothing in reach
+    # more query tiles than SMs
+    ((5, 17, 23, 12, 128, 0.8, 2), N_ | B_, 2, 3, 4),
+    ((5, 17, 23, 12, 64, 0.8, 2), 0, 1, 3, 3),
+    ((5, 17, 23, 12, 128, 0.8, 2), Q_ | N_ | D_ | tra.tra_flag_tile_w(8), 1, 3, 5),
+    ((6, 17, 23, 12, 64, 0.8, 1), Q_ | B_ | tra.tra_flag_tile_w(8), 3, 3, 4),
+    ((7, 12, 11, 60, 64, 0.8, 2), N_, 5, 2, 3),          # and the last query frame reaches no cached frame
 ]
 
 
