@@ -362,7 +362,9 @@ TRA_API tra_status tra_cache_attention_bytes(tra_plan plan, int n_frames, size_t
  *   out      device [heads][n][d], fp32 (bf16 with TRA_FLAG_OUT_BF16)
  *   lse      device fp32 [heads][n]; zeros and -infinity where no cached key
  *            is kept
- * n = 0 does nothing.  All arithmetic is fp32.  Asynchronous on `stream`.
+ * n = 0 does nothing.  To fp32 accuracy: scores and sums are fp32, and where many
+ * tokens run on the tensor cores the weights of v are two f16 parts each.
+ * Asynchronous on `stream`.
  */
 TRA_API tra_status tra_cache_attention_tokens(tra_plan plan, const void* q, const int32_t* token,
                          const int32_t* radius, int n, const void* cache, size_t cache_bytes,

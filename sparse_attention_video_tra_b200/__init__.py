@@ -489,7 +489,8 @@ class Plan:
         if cache.dtype is not torch.uint8 or not cache.is_contiguous() or cache.numel() < c.cache_bytes:
             raise ValueError(f"cache: expected contiguous uint8 with {c.cache_bytes} elements, got {cache.dtype} "
                              f"{tuple(cache.shape)}")
-        cache = cache.view(-1)[:c.cache_bytes]
+        if cache.dim() != 1 or cache.numel() != c.cache_bytes:
+            cache = cache.view(-1)[:c.cache_bytes]
         codes, scale = cache.view(torch.float8_e4m3fn), cache.view(torch.float32)
         shape, strides = (i.heads, i.n_tiles, 128, i.d), (i.N_pad * i.d, 128 * i.d, i.d, 1)
         first = cache.storage_offset()

@@ -110,7 +110,7 @@ constexpr uint32_t MT_IN0 = 1u << 26, MT_FULL0 = 1u << 28;
 // of the key frames [k0, k1) only.
 struct Span {
     int q0, nq, k0, k1;
-    int parts;                   // LONE: CTAs of the cluster that shares a tile's keys
+    int parts;                   // LONE: CTAs of the cluster that shares a tile's keys; 0: one chain takes all
 };
 
 // LSE: also write each row's log-sum-exp (natural log) to `lse`; O is then
@@ -119,10 +119,11 @@ struct Span {
 // listed key tiles outside them are passed over, and a row that is left with
 // no key gets zeros and -inf.
 // LONE (with LSE), for grids that leave SMs idle: one query tile (slot) per CTA,
-// or per cluster of two or four CTAs that take a part of its key tiles each and
-// join their O, maxima and sums through distributed shared memory.  The chain
-// of a lone tile takes 1.9 us a key tile, that of a pair 2.5 us; 3 frames of
-// 17 x 23 over 6, 4 heads: 78 us in pairs, 60 us alone, 39 us in clusters of two.
+// or per cluster of two or four CTAs.  The CTA's two chains take the tile's key
+// tiles in turn, the CTAs of a cluster a part of them each, and O, maxima and
+// sums are joined through (distributed) shared memory (3 frames of 17 x 23 over
+// 6, 4 heads: 78 us with two tiles per CTA, 60 us with one chain per tile, 32 us
+// so).  For a few key tiles one chain takes them all: the join costs 3 us.
 template <int D, int TWL, bool OUT_BF16, bool DISK, bool LSE, bool SPAN, bool LONE>
 __global__ void __launch_bounds__(384, 1)
 attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -176,12 +177,13 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         qa = (q0 + nq - 1) * tpf + 2 * (pair - paired);
         qb = qa + 1;
     }
-    const int parts = LONE ? span.parts : 1, part = LONE ? pair % parts : 0;
+    const bool shared = LONE && span.parts > 0;         // both chains work on one tile
+    const int parts = shared ? span.parts : 1, part = shared ? pair % parts : 0;
     if (LONE) {
         qa = q0 * tpf + pair / parts;
-        qb = qa + 1;
+        qb = shared ? qa : qa + 1;
     }
-    const bool hasB = !LONE && qb < (q0 + nq) * tpf;
+    const bool hasB = (!LONE || shared) && qb < (q0 + nq) * tpf;
     // the row of token (t, h, w) in q, out and lse
     auto query_row = [&](int t, int h, int w, int tile_row) -> size_t {
         if constexpr (SPAN)
@@ -209,7 +211,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     };
     const int32_t* counts = reinterpret_cast<const int32_t*>(mask + G.off_count) + (size_t)g * G.nQ;
     const uint16_t* lists = reinterpret_cast<const uint16_t*>(mask + G.off_list) + (size_t)g * G.nQ * G.list_cap;
-    int nA = counts[qa], nB = hasB ? counts[qb] : 0;
+    int nA = counts[qa], nB = hasB && !shared ? counts[qb] : 0;
     // the mask buffer is caller memory: a count outside [0, list_cap] is an
     // error (recorded; this CTA then does nothing)
     if (nA < 0 || nA > G.list_cap || nB < 0 || nB > G.list_cap) {
@@ -225,8 +227,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     for (int i = tid; i < 7 * L.bw; i += C::THREADS) bits[i] = 0;
     __syncthreads();
     for (int i = tid; i < nA + nB; i += C::THREADS) {
-        const bool isB = i >= nA;
-        const int e = isB ? lists[(size_t)qb * G.list_cap + (i - nA)] : lists[(size_t)qa * G.list_cap + i];
+        const bool isB = shared ? (i & 1) != 0 : i >= nA;   // a shared tile's entries in turn
+        const int e = isB && !shared ? lists[(size_t)qb * G.list_cap + (i - nA)] : lists[(size_t)qa * G.list_cap + i];
         const int bit = (e & 0x7fff) - base;
         // a key tile its own query tile cannot reach (outside the grid, or more
         // than Rt' frames from that tile's frame) is an error: recorded, skipped
@@ -560,7 +562,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_wait(&drain[w], 0, G.drain_ns);
         }
       }
-      if (LONE && parts > 1) {
+      if (shared) {
           __syncwarp();
           cluster_sync();
           cluster_sync();
@@ -744,32 +746,33 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_arrive(&p_full[w]);
             ++k;
         }
-        if (LONE && parts > 1) {
+        if (shared) {
             if (ok && k > 0) ok = role_wait(&pv_done[w], (k - 1) & 1, G.wait_ns, s_abort);
             ok = __all_sync(0xffffffffu, ok);
-            if (active) {
-                // unnormalised O, its maximum and sum into this CTA's shared memory (Q, K
-                // and V are done with); 16-byte chunks of a row swizzled over the banks
-                tc_fence_after();
-                __syncwarp();
-                float4* po = reinterpret_cast<float4*>(smem) + row * (D / 4);
+            // both chains are through with Q, K and V: their places take each chain's
+            // unnormalised O (16-byte chunks of a row swizzled over the banks), then
+            // the rows' maxima and sums
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            constexpr int PART = 128 * D * 4;
+            tc_fence_after();
+            __syncwarp();
+            float4* po = reinterpret_cast<float4*>(smem + w * PART) + row * (D / 4);
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t v[32];
-                    if (ok && k > 0) {
-                        tmem_ld32(tmem + lane_base + colO + c * 32, v);
-                        tmem_wait_ld();
-                    } else {
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                if (ok && k > 0) {
+                    tmem_ld32(tmem + lane_base + colO + c * 32, v);
+                    tmem_wait_ld();
+                } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0u;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        po[(c * 8 + i) ^ (row & 7)] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                                                  __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                    for (int i = 0; i < 32; ++i) v[i] = 0u;
                 }
-                reinterpret_cast<float2*>(smem + 128 * D * 4)[row] = make_float2(m_run, ok && k > 0 ? l : 0.f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    po[(c * 8 + i) ^ (row & 7)] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                              __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
             }
+            reinterpret_cast<float2*>(smem + 2 * PART)[w * 128 + row] = make_float2(m_run, ok && k > 0 ? l : 0.f);
             cluster_sync();
             // each CTA joins its share of the rows: 8 warps, a thread per 16-byte chunk
             const int rows = 128 / parts;
@@ -777,10 +780,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const int r = part * rows + e / (D / 4), ch = e % (D / 4);
                 float mj = -INFINITY, lj = 0.f;
                 float4 oj = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int p = 0; p < parts; ++p) {
-                    const float2 ml = cluster_load_f2(smem + 128 * D * 4 + r * 8, p);
+                for (int p = 0; p < 2 * parts; ++p) {
+                    const float2 ml = cluster_load_f2(smem + 2 * PART + ((p & 1) * 128 + r) * 8, p >> 1);
                     if (ml.y == 0.f) continue;              // this part kept no key
-                    const float4 o = cluster_load_f4(smem + (r * (D / 4) + (ch ^ (r & 7))) * 16, p);
+                    const float4 o = cluster_load_f4(smem + (p & 1) * PART + (r * (D / 4) + (ch ^ (r & 7))) * 16, p >> 1);
                     const float mn = fmaxf(mj, ml.x), a = ex2(mj - mn), b = ex2(ml.x - mn);
                     lj = lj * a + ml.y * b;
                     oj = make_float4(oj.x * a + o.x * b, oj.y * a + o.y * b, oj.z * a + o.z * b, oj.w * a + o.w * b);

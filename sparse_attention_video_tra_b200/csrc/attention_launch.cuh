@@ -44,11 +44,12 @@ tra_status run_attention(const tra::Geom& G, const CUtensorMap& q, const CUtenso
     if constexpr (LSE) {
         const long long all = (long long)tiles * G.G;
         if (all <= kSMs) {
-            // two or four CTAs per tile where they all run at once and have four key tiles or more each
+            // more than eight key tiles: both chains, and two or four CTAs per tile where they
+            // all run at once and have eight key tiles or more each
             tra::Span sp = span;
-            sp.parts = 1;
-            while (sp.parts < 4 && all * 2 * sp.parts <= kSMs && G.list_cap >= 8 * sp.parts) sp.parts *= 2;
-            return launch_attention<D, TWL, OB, DISK, LSE, SPAN, true>(G, q, k, v, mask, out, qraw, lse, sp, tiles * sp.parts, st);
+            sp.parts = G.list_cap > 8 ? 1 : 0;
+            while (sp.parts && sp.parts < 4 && all * 2 * sp.parts <= kSMs && G.list_cap >= 16 * sp.parts) sp.parts *= 2;
+            return launch_attention<D, TWL, OB, DISK, LSE, SPAN, true>(G, q, k, v, mask, out, qraw, lse, sp, tiles * std::max(1, sp.parts), st);
         }
     }
     // two query tiles per CTA; with radius-sorted groups, the same slot of
