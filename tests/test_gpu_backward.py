@@ -315,6 +315,24 @@ def test_bounded_waits_of_the_training_kernels_give_up():
     assert s.plan.status() == 0
 
 
+@pytest.mark.parametrize("grid", [(4, 8, 8, 2), (9, 24, 10, 1), (5, 17, 23, 2), (5, 17, 23, 8)])
+def test_bounded_waits_of_the_forward_variants_give_up(grid):
+    """One chain, clusters of four and two CTAs per tile, and pairs of tiles: each ends and reports the timeout."""
+    T, H, W, heads = grid
+    s = Setup(T, H, W, heads, 64, 0.9, 8, N_)
+    want = [x.clone() for x in s.forward()]
+    torch.cuda.synchronize()
+    assert s.plan.status() == 0
+    p = tra.Plan(T, H, W, heads, 64, 1.0, 0.5, 0.9, 8, 1, N_ | tra.TRA_FLAG_DEBUG_NO_WAIT)
+    p.attention_lse(s.q, s.k, s.v, s.mask, p.new_out(), p.new_lse())
+    torch.cuda.synchronize()
+    assert p.status() == 5                              # TRA_ERR_TIMEOUT
+    got = s.forward()
+    torch.cuda.synchronize()
+    assert s.plan.status() == 0
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 def test_refusals():
     s = Setup(4, 8, 8, 2, 64, 0.7, 2, N_)
     out, lse = s.forward()
