@@ -124,19 +124,20 @@ extern "C" tra_status tra_cache_attention_tokens(tra_plan plan, const void* q, c
     if (cache_bytes < cache_layout(G).cache_bytes) return TRA_ERR_WORKSPACE;
     const long long units = (long long)n * G.G;
     if (units > (1ll << 31) - 1) return TRA_ERR_UNSUPPORTED;
-    // Groups of 16 tokens share a key's codes on the tensor cores once that fills
-    // the card; below, one token at a time over more CTAs.  Measured cold, one
-    // token at a time / grouped: 45 / 53 us for 1 token and 40 heads at
-    // 21 x 45 x 80, 121 / 64 for 2 and 338 / 86 for 16; 39 / 28 for 6 tokens and
-    // 12 heads at 21 x 30 x 52, but 27 / 23 for 4 and 12 / 16 for 8 tokens and 4
-    // heads at 9 x 17 x 23.
-    const bool grouped = n >= 2 && units >= 64;
+    // Groups of 16 tokens share a key's codes on the tensor cores once enough of a
+    // group's rows are filled and there is work for the card; below, one token at
+    // a time over more CTAs.  Measured cold, one token at a time / grouped: with 40
+    // heads at 21 x 45 x 80 50 / 87 us for 2 tokens, 89 / 93 for 4, 91 / 83 for 6
+    // and 159 / 91 for 16; with 12 heads at 21 x 30 x 52 22 / 30 us for 2, 26 / 26
+    // for 4 and 34 / 28 for 8; with 4 heads at 9 x 17 x 23 11 / 17 us for 8 and
+    // 17 / 19 for 16.
+    const bool grouped = n >= 6 && units >= 64;
     const long long work = grouped ? (long long)((n + tra::GROUP - 1) / tra::GROUP) * G.G : units;
     // CTAs per group or token and head, a cluster.  Groups run one CTA per SM: the
     // most that all run at once, counting that a cluster lies within one GPC and
     // large ones leave SMs over (24 clusters of 5: 41 us, of 6: 59 us; 48 of
     // 3: 65 us, of 4: 72 us).  Lone tokens: as many as stay resident together, 16
-    // (35 -> 26 us for 1 token and 12 heads) while they cost no other its place.
+    // (a quarter faster for 1 token and 12 heads) while they cost no other its place.
     int csize = 8;
     if (grouped) {
         while (csize > 2 && work * csize > (csize > 4 ? 128 : 144)) --csize;
