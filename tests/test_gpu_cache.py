@@ -301,6 +301,44 @@ def test_token_outside_the_grid_is_reported_and_its_rows_left():
     s.ok()
 
 
+@pytest.mark.parametrize("n", [1, 4, 5, 6, 7, 15, 16, 33])
+@pytest.mark.parametrize("d,flags", [(64, N_ | D_), (128, N_)])
+def test_few_tokens_of_many_heads(n, d, flags):
+    """Around the number of tokens from which they are taken in groups; the last row's token is the grid's last."""
+    s = Setup(4, 11, 19, 13, d, 0.85, 2, flags)
+    s.store()
+    g = torch.Generator(device="cuda").manual_seed(n)
+    token = torch.randint(0, s.i.N, (n,), generator=g, device="cuda", dtype=torch.int32)
+    token[-1] = s.i.N - 1
+    radius = torch.randint(0, 20, (13, n), generator=g, device="cuda", dtype=torch.int32)
+    out, lse = s.tokens(token, radius, 4)
+    s.ok()
+    keep = ref.pairs_kept(4, 11, 19, 0.85, 2, token.long(), torch.arange(s.i.N, device="cuda"), radius, bool(flags & D_))
+    o, l, oe, le = ref.attention(s.q[:, token.long()], *s.held(), keep, 0.0)
+    ref.check(out, o, oe + 2.0 ** -18 * o.abs(), "out")
+    ref.check(lse, l, le, "lse")
+
+
+def test_tokens_outside_the_grid_among_many_are_reported_and_their_rows_left():
+    s = Setup(4, 8, 8, 2, 64, 0.7, 2, N_)
+    s.store()
+    g = torch.Generator(device="cuda").manual_seed(6)
+    token = torch.randint(0, s.i.N, (50,), generator=g, device="cuda", dtype=torch.int32)
+    radius = torch.full((2, 50), 3, dtype=torch.int32, device="cuda")
+    whole, whole_lse = s.tokens(token, radius, 4)
+    s.ok()
+    bad = token.clone()
+    bad[0], bad[17], bad[49] = s.i.N, 2 ** 31 - 1, -2 ** 31
+    out, lse = s.tokens(bad, radius, 4, s.q[:, token.long()].contiguous())
+    torch.cuda.synchronize()
+    assert s.plan.status() == 6                          # TRA_ERR_DEVICE_CHECK
+    left = torch.zeros(50, dtype=torch.bool, device="cuda")
+    left[[0, 17, 49]] = True
+    assert (out[:, left] == 7).all() and (lse[:, left] == 7).all()
+    assert torch.equal(out[:, ~left], whole[:, ~left]) and torch.equal(lse[:, ~left], whole_lse[:, ~left])
+    s.ok()
+
+
 @pytest.mark.parametrize("flags", [0, N_ | B_, N_ | D_])
 def test_generating_a_clip_frame_by_frame(flags):
     """Store, then attend, one frame after the other; single tokens agree with the frame's rows, and the parts of a
