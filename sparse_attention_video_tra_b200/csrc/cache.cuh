@@ -10,7 +10,6 @@
 #pragma once
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 #include "pipeline.cuh"
 
@@ -396,17 +395,18 @@ token_attention_kernel(const Geom G, const CacheView C, const uint4* __restrict_
 //   S = Q K^T   two 8-key column tiles, d/16 K steps.  The order of the d
 //               elements along K is free as long as Q and K agree: lane c of a
 //               quad takes the 16-code chunks c (and c + 4), word by word.
-//   softmax     running maximum per row (raised when exceeded by 2^8) and sum
-//               of the unrounded P; the weights of V are split into two f16
-//               parts, so nothing is rounded beyond 2^-22.
+//   softmax     running maximum and sum of the unrounded P per row, in fp32
 //   O += P V    d/8 column tiles.  Column n of tile j is the d element
 //               (d/8) n + j, so the lane needs byte j of four key rows, and each
-//               pair of keys is one byte permute of two words.
-// The products run in f16, which holds every code, and one instruction turns two
+//               pair of keys is one byte permute of two words.  The weight of a
+//               code, P times the V scale, is split into three bf16 parts: 24
+//               bits over fp32's whole range, so tiles of any scales may meet
+//               in a row (two f16 parts in a frame that follows the scales cost
+//               an eighth less time, but lose the tiles far below it).
+// The scores run in f16, which holds every code, and one instruction turns two
 // codes into f16.  Q is scaled by a power of two per row to at most 2^15 (its 8
 // bits stay exact down to 2^-28 of the row's largest element; below, the error
-// is 2^-40 of that).  O has a frame of its own: the weights that multiply
-// codes are P times the V scale over 2^mv, kept below 2^15 by raising mv.
+// is 2^-40 of that).
 __device__ __forceinline__ uint32_t codes_to_f16x2(uint32_t x)       // codes in bytes 0 and 1
 {
     uint32_t r;
@@ -424,6 +424,21 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// the same as bf16, exact
+__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t x)
+{
+    float l, h;
+    asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(l), "=f"(h) : "r"(codes_to_f16x2(x)));
+    return pack_bf16x2(l, h);
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -538,7 +553,6 @@ token_group_kernel(const Geom G, const CacheView C, const uint32_t* __restrict__
 #pragma unroll
     for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};     // P is relative to 2^m
-    float mv[2] = {-INFINITY, -INFINITY};                       // O to 2^mv
     const int gw_log2 = min(G.tw_log2, 4), gr_log2 = 4 - gw_log2;       // a granule: 2^gr_log2 x 2^gw_log2 keys
     // A granule belongs to one of the cluster's warps by its number in the frame
     // alone, not by the group's boxes: a row's sums run in the same order
@@ -677,33 +691,29 @@ token_group_kernel(const Geom G, const CacheView C, const uint32_t* __restrict__
                 mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
                 mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
             }
-            const float lv = log2f(vs);                      // an integer
-            uint32_t ph[4], pl[4];
-            bool raise = false;
+            uint32_t ph[4], pm[4], pl[4];                    // the weights' parts
             float al[2] = {1.f, 1.f};
+            bool raise = false;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                if (mx[x] > m[x] + 8.f) {                    // -inf + 8: the first kept key
-                    l[x] *= m[x] == -INFINITY ? 0.f : ex2(m[x] - mx[x]);
+                if (mx[x] > m[x]) {
+                    al[x] = ex2(m[x] - mx[x]);               // 0 for the first kept key
+                    l[x] *= al[x];
                     m[x] = mx[x];
-                }
-                // the weights' frame, raised where this granule's would pass 2^15
-                if (mx[x] > -INFINITY && m[x] + lv > mv[x] + 7.f) {
-                    al[x] = mv[x] == -INFINITY ? 0.f : ex2(mv[x] - (m[x] + lv));
-                    mv[x] = m[x] + lv;
                     raise = true;
                 }
                 const float base = m[x] == -INFINITY ? 0.f : m[x];
-                const float wv = mx[x] > -INFINITY ? ex2(m[x] + lv - mv[x]) : 0.f;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float a = ex2(p[x][2 * j] - base), b = ex2(p[x][2 * j + 1] - base);
                     l[x] += a + b;
-                    const float av = a * wv, bv = b * wv;
-                    const uint32_t hi = pack_f16x2(av, bv);
-                    const __half2 h2 = *reinterpret_cast<const __half2*>(&hi);
+                    const float av = a * vs, bv = b * vs;
+                    const uint32_t hi = pack_bf16x2(av, bv);
+                    const float ar = av - __uint_as_float(hi << 16), br = bv - __uint_as_float(hi & 0xffff0000u);
+                    const uint32_t mid = pack_bf16x2(ar, br);
                     ph[2 * j + x] = hi;
-                    pl[2 * j + x] = pack_f16x2(av - __low2float(h2), bv - __high2float(h2));
+                    pm[2 * j + x] = mid;
+                    pl[2 * j + x] = pack_bf16x2(ar - __uint_as_float(mid << 16), br - __uint_as_float(mid & 0xffff0000u));
                 }
             }
             if (__any_sync(0xffffffffu, raise)) {
@@ -719,10 +729,11 @@ token_group_kernel(const Geom G, const CacheView C, const uint32_t* __restrict__
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const uint32_t sel = (uint32_t)((j & 3) | ((4 + (j & 3)) << 4));
-                const uint32_t b0 = codes_to_f16x2(__byte_perm(vv[0][j >> 2], vv[1][j >> 2], sel));
-                const uint32_t b1 = codes_to_f16x2(__byte_perm(vv[2][j >> 2], vv[3][j >> 2], sel));
-                mma_f16(o[j], ph, b0, b1);
-                mma_f16(o[j], pl, b0, b1);
+                const uint32_t b0 = codes_to_bf16x2(__byte_perm(vv[0][j >> 2], vv[1][j >> 2], sel));
+                const uint32_t b1 = codes_to_bf16x2(__byte_perm(vv[2][j >> 2], vv[3][j >> 2], sel));
+                mma_bf16(o[j], pl, b0, b1);
+                mma_bf16(o[j], pm, b0, b1);
+                mma_bf16(o[j], ph, b0, b1);
             }
         }
     }
@@ -736,11 +747,10 @@ token_group_kernel(const Geom G, const CacheView C, const uint32_t* __restrict__
             s_m[warp][r0 + 8 * x] = m[x];
             s_l[warp][r0 + 8 * x] = l[x];
         }
-        const float back = m[x] == -INFINITY ? 0.f : ex2(mv[x] - m[x]);     // O into the frame of m
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            s_o[warp][r0 + 8 * x][2 * c * NT + j] = o[j][2 * x] * back;
-            s_o[warp][r0 + 8 * x][(2 * c + 1) * NT + j] = o[j][2 * x + 1] * back;
+            s_o[warp][r0 + 8 * x][2 * c * NT + j] = o[j][2 * x];
+            s_o[warp][r0 + 8 * x][(2 * c + 1) * NT + j] = o[j][2 * x + 1];
         }
     }
     __syncthreads();

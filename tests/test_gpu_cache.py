@@ -503,3 +503,71 @@ def test_refusals():
         with pytest.raises(ValueError):
             call()
     s.ok()
+
+
+def wide_scale_tokens(change, n, d=128, heads=12, q=None):
+    """n neighbouring tokens of frame 6 over 13 cached 30x52 frames, k and v as `change` makes them: (setup, tokens,
+    their queries, the kept pairs, out, lse).  A warp of the grouped form walks dozens of granules there."""
+    s = Setup(13, 30, 52, heads, d, 0.9, 6, N_)
+    change(s)
+    s.store()
+    g = torch.Generator(device="cuda").manual_seed(n)
+    token = 6 * 30 * 52 + 400 + torch.arange(n, device="cuda", dtype=torch.int32)
+    radius = torch.randint(6, 20, (heads, n), generator=g, device="cuda", dtype=torch.int32)
+    q = s.q[:, token.long()].contiguous() if q is None else q(s.q[:, token.long()].contiguous())
+    out, lse = s.tokens(token, radius, 13, q)
+    s.ok()
+    keep = ref.pairs_kept(13, 30, 52, 0.9, 6, token.long(), torch.arange(s.i.N, device="cuda"), radius)
+    return s, q, keep, out, lse
+
+
+def frame_of(s):
+    return torch.arange(s.i.N, device="cuda") // (30 * 52)
+
+
+@pytest.mark.parametrize("n,d", [(5, 128), (6, 128), (52, 128), (16, 64)])
+@pytest.mark.parametrize("bits", [-6, -10, -13, -17])
+def test_tokens_over_a_frame_of_zero_values(n, d, bits):
+    """Tiles of zeros have the scale 2^0: they must not cost the small values of the other frames their bits."""
+    def change(s):
+        s.v.mul_(2.0 ** bits)
+        s.v[:, frame_of(s) == 0] = 0
+    s, q, keep, out, lse = wide_scale_tokens(change, n, d)
+    o, l, oe, le = ref.attention(q, *s.held(), keep, 2.0 ** -20)
+    ref.check(out, o, oe, "out")
+    ref.check(lse, l, le, "lse")
+
+
+@pytest.mark.parametrize("n,d", [(5, 128), (6, 128), (52, 128), (16, 64)])
+@pytest.mark.parametrize("bits", [16, 20])
+def test_tokens_over_a_frame_of_large_values_at_low_scores(n, d, bits):
+    """One frame's values are 2^bits larger and its scores 30 bits lower: its weights do not set the others' accuracy."""
+    def change(s):
+        at = frame_of(s) == 1
+        s.k[..., 0] = 0
+        s.k[:, at, 0] = -30 * math.log(2) * math.sqrt(d) / 8
+        s.v[:, at] *= 2.0 ** bits
+
+    def query(q):
+        q[..., 0] = 8
+        return q
+    s, q, keep, out, lse = wide_scale_tokens(change, n, d, q=query)
+    o, l, oe, le = ref.attention(q, *s.held(), keep, 2.0 ** -20)
+    ref.check(out, o, oe, "out")
+    ref.check(lse, l, le, "lse")
+
+
+@pytest.mark.parametrize("n,d", [(5, 128), (6, 128), (52, 128), (16, 64)])
+@pytest.mark.parametrize("large", [0, 12])
+def test_tokens_over_an_outlier_channel_of_one_frame(n, d, large):
+    """The large frame, first or last, fills one channel only: the other channels come from the small frames and carry
+    a bound of their own size."""
+    def change(s):
+        at = frame_of(s) == large
+        s.v[:, at, 1:] = 0
+        s.v[:, at, 0] *= 2.0 ** 20
+        s.v[:, ~at, 0] = 0
+    s, q, keep, out, lse = wide_scale_tokens(change, n, d)
+    o, l, oe, le = ref.attention(q, *s.held(), keep, 2.0 ** -20)
+    ref.check(out, o, oe, "out")
+    ref.check(lse, l, le, "lse")
