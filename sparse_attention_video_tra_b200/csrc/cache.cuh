@@ -403,36 +403,16 @@ token_attention_kernel(const Geom G, const CacheView C, const uint4* __restrict_
 //               bits over fp32's whole range, so tiles of any scales may meet
 //               in a row (two f16 parts in a frame that follows the scales cost
 //               an eighth less time, but lose the tiles far below it).
-// The scores run in f16, which holds every code, and one instruction turns two
-// codes into f16.  Q is scaled by a power of two per row to at most 2^15 (its 8
-// bits stay exact down to 2^-28 of the row's largest element; below, the error
-// is 2^-40 of that).
-__device__ __forceinline__ uint32_t codes_to_f16x2(uint32_t x)       // codes in bytes 0 and 1
+// Both products run in bf16: it holds every code, and Q as it comes.  (f16 takes
+// two instructions less per pair of codes, a twentieth of the time, but there a
+// Q row has to be scaled to f16's range, and its elements 2^33 below the largest
+// one are lost beside it, also where that one meets keys of zero.)
+__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t x)      // codes in bytes 0 and 1; exact
 {
     uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)x));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// the same as bf16, exact
-__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t x)
-{
     float l, h;
-    asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(l), "=f"(h) : "r"(codes_to_f16x2(x)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)x));
+    asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(l), "=f"(h) : "r"(r));
     return pack_bf16x2(l, h);
 }
 
@@ -517,35 +497,19 @@ token_group_kernel(const Geom G, const CacheView C, const uint32_t* __restrict__
     // ---- this lane's rows r0, r0 + 8 of the group and its share of Q
     const int c = lane & 3, r0 = lane >> 2;
     uint32_t qa[KS][4];
-    float q_unit[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int i = first + r0 + 8 * x;
         const bool ok = i < n && s_t[r0 + 8 * x] >= 0;
         const uint4* src = reinterpret_cast<const uint4*>(q + ((size_t)g * n + (ok ? i : 0)) * (D / 2));
-        uint32_t w[CH][8], most = 0;                         // the lane's d elements and their largest magnitude (bf16 bits)
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             // d elements 16 (c + 4k) .. + 15: K steps 4k .. 4k + 3
             const uint4 a = __ldg(src + 2 * (c + 4 * k)), b = __ldg(src + 2 * (c + 4 * k) + 1);
             const uint32_t w8[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                w[k][s] = ok ? w8[s] : 0u;
-                most = max(most, max(w[k][s] & 0x7fffu, (w[k][s] >> 16) & 0x7fffu));
-            }
+            for (int s = 0; s < 8; ++s) qa[4 * k + (s >> 1)][(s & 1) * 2 + x] = ok ? w8[s] : 0u;
         }
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        // 2^(14 - E) for a largest element of 1.f * 2^E, within what fp32 can undo
-        const int shift = min(max(14 - ((int)(most >> 7) - 127), -112), 126);
-        const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
-        q_unit[x] = __uint_as_float((uint32_t)(127 - shift) << 23);
-#pragma unroll
-        for (int k = 0; k < CH; ++k)
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-                qa[4 * k + (s >> 1)][(s & 1) * 2 + x] = pack_f16x2(__uint_as_float(w[k][s] << 16) * up, __uint_as_float(w[k][s] & 0xffff0000u) * up);
     }
     const int t0 = s_t[r0], t1 = s_t[r0 + 8], qh0 = s_h[r0], qh1 = s_h[r0 + 8], qw0 = s_w[r0], qw1 = s_w[r0 + 8];
 
@@ -674,15 +638,15 @@ token_group_kernel(const Geom G, const CacheView C, const uint32_t* __restrict__
                     const uint32_t w4[4] = {kk[j][k].x, kk[j][k].y, kk[j][k].z, kk[j][k].w};
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
-                        mma_f16(sc[j], qa[4 * k + s], codes_to_f16x2(w4[s]), codes_to_f16x2(w4[s] >> 16));
+                        mma_bf16(sc[j], qa[4 * k + s], codes_to_bf16x2(w4[s]), codes_to_bf16x2(w4[s] >> 16));
                 }
             }
             // ---- softmax; p[x][2 j + k] of row x
             float p[2][4];
             float mx[2] = {-INFINITY, -INFINITY};
+            const float unit = ks * G.scale_log2;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const float unit = ks * q_unit[x] * G.scale_log2;
 #pragma unroll
                 for (int jk = 0; jk < 4; ++jk) {
                     p[x][jk] = (keep >> (4 * x + jk)) & 1u ? sc[jk >> 1][2 * x + (jk & 1)] * unit : -INFINITY;

@@ -571,3 +571,36 @@ def test_tokens_over_an_outlier_channel_of_one_frame(n, d, large):
     o, l, oe, le = ref.attention(q, *s.held(), keep, 2.0 ** -20)
     ref.check(out, o, oe, "out")
     ref.check(lse, l, le, "lse")
+
+
+@pytest.mark.parametrize("n,d", [(5, 128), (6, 128), (52, 128), (16, 64)])
+@pytest.mark.parametrize("bits", [20, 34, 40, 90])
+def test_tokens_whose_queries_have_an_outlier(n, d, bits):
+    """One element of each query is 2^bits where the keys are zeros: the scores come from the others, in full."""
+    def change(s):
+        s.k[..., 0] = 0
+
+    def query(q):
+        q[..., 0] = 2.0 ** bits
+        return q
+    s, q, keep, out, lse = wide_scale_tokens(change, n, d, q=query)
+    o, l, oe, le = ref.attention(q, *s.held(), keep, 2.0 ** -20)
+    ref.check(out, o, oe, "out")
+    ref.check(lse, l, le, "lse")
+
+
+@pytest.mark.parametrize("n", [5, 40])
+def test_tokens_with_large_queries_over_large_keys_that_do_not_meet(n):
+    """Queries of 2^90 in one element, keys of 2^60 in another one: every score is zero, every output the mean value."""
+    def change(s):
+        s.k.zero_()
+        s.k[..., 1] = 2.0 ** 60
+
+    def query(q):
+        q.zero_()
+        q[..., 0] = 2.0 ** 90
+        return q
+    s, q, keep, out, lse = wide_scale_tokens(change, n, q=query)
+    o, l, oe, le = ref.attention(q, *s.held(), keep, 2.0 ** -20)
+    ref.check(out, o, oe, "out")
+    ref.check(lse, l, le, "lse")
