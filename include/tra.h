@@ -358,6 +358,8 @@ TRA_API tra_status tra_cache_attention_bytes(tra_plan plan, int n_frames, size_t
  *            (any order, repeats allowed).  A negative index marks an unused
  *            place: its rows of out and lse are left as they were.  An index of
  *            N or more is recorded as TRA_ERR_DEVICE_CHECK and treated likewise.
+ *            From 8 tokens on, 16 consecutive places share the keys they read:
+ *            best in the order of the grid, so that they are neighbours.
  *   radius   device int32 [heads][n], 0 or more; a negative radius keeps no key
  *   out      device [heads][n][d], fp32 (bf16 with TRA_FLAG_OUT_BF16)
  *   lse      device fp32 [heads][n]; zeros and -infinity where no cached key

@@ -126,12 +126,16 @@ extern "C" tra_status tra_cache_attention_tokens(tra_plan plan, const void* q, c
     if (units > (1ll << 31) - 1) return TRA_ERR_UNSUPPORTED;
     // Groups of 16 tokens share a key's codes on the tensor cores once enough of a
     // group's rows are filled and there is work for the card; below, one token at
-    // a time over more CTAs.  Measured cold, one token at a time / grouped: with 40
-    // heads at 21 x 45 x 80 50 / 87 us for 2 tokens, 89 / 93 for 4, 91 / 83 for 6
-    // and 159 / 91 for 16; with 12 heads at 21 x 30 x 52 22 / 30 us for 2, 26 / 26
-    // for 4 and 34 / 28 for 8; with 4 heads at 9 x 17 x 23 11 / 17 us for 8 and
-    // 17 / 19 for 16.
-    const bool grouped = n >= 6 && units >= 64;
+    // a time over more CTAs.  Measured cold on neighbouring tokens, one token at a
+    // time / grouped: with 40 heads at 21 x 45 x 80 88 / 94 us for 6 tokens,
+    // 168 / 102 for 8 and 154 / 102 for 16; with 12 heads at 21 x 30 x 52 31 / 29 us
+    // for 8 and 47 / 33 for 16.  With few heads: 4 at 21 x 45 x 80 41 / 49 us for 16,
+    // 49 / 49 for 24, 61 / 45 for 48; 2 at 21 x 30 x 52 25 / 31 us for 32, 31 / 33 for
+    // 48, 29 / 29 for 64; 4 at 9 x 17 x 23 16 / 16 us for 8 to 32, 20 / 18 for 64.
+    // (Tokens scattered over the clip share few keys and are faster one at a time,
+    // 162 against 283 us for 64 of 12 heads, but where they lie is known on the
+    // device only.)
+    const bool grouped = n >= 8 && units >= 96;
     const long long work = grouped ? (long long)((n + tra::GROUP - 1) / tra::GROUP) * G.G : units;
     // CTAs per group or token and head, a cluster.  Groups run one CTA per SM: the
     // most that all run at once, counting that a cluster lies within one GPC and

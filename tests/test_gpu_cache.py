@@ -525,7 +525,7 @@ def frame_of(s):
     return torch.arange(s.i.N, device="cuda") // (30 * 52)
 
 
-@pytest.mark.parametrize("n,d", [(5, 128), (6, 128), (52, 128), (16, 64)])
+@pytest.mark.parametrize("n,d", [(5, 128), (6, 128), (8, 128), (52, 128), (16, 64)])
 @pytest.mark.parametrize("bits", [-6, -10, -13, -17])
 def test_tokens_over_a_frame_of_zero_values(n, d, bits):
     """Tiles of zeros have the scale 2^0: they must not cost the small values of the other frames their bits."""
@@ -538,7 +538,7 @@ def test_tokens_over_a_frame_of_zero_values(n, d, bits):
     ref.check(lse, l, le, "lse")
 
 
-@pytest.mark.parametrize("n,d", [(5, 128), (6, 128), (52, 128), (16, 64)])
+@pytest.mark.parametrize("n,d", [(5, 128), (6, 128), (8, 128), (52, 128), (16, 64)])
 @pytest.mark.parametrize("bits", [16, 20])
 def test_tokens_over_a_frame_of_large_values_at_low_scores(n, d, bits):
     """One frame's values are 2^bits larger and its scores 30 bits lower: its weights do not set the others' accuracy."""
@@ -557,7 +557,7 @@ def test_tokens_over_a_frame_of_large_values_at_low_scores(n, d, bits):
     ref.check(lse, l, le, "lse")
 
 
-@pytest.mark.parametrize("n,d", [(5, 128), (6, 128), (52, 128), (16, 64)])
+@pytest.mark.parametrize("n,d", [(5, 128), (6, 128), (8, 128), (52, 128), (16, 64)])
 @pytest.mark.parametrize("large", [0, 12])
 def test_tokens_over_an_outlier_channel_of_one_frame(n, d, large):
     """The large frame, first or last, fills one channel only: the other channels come from the small frames and carry
@@ -573,7 +573,7 @@ def test_tokens_over_an_outlier_channel_of_one_frame(n, d, large):
     ref.check(lse, l, le, "lse")
 
 
-@pytest.mark.parametrize("n,d", [(5, 128), (6, 128), (52, 128), (16, 64)])
+@pytest.mark.parametrize("n,d", [(5, 128), (6, 128), (8, 128), (52, 128), (16, 64)])
 @pytest.mark.parametrize("bits", [20, 34, 40, 90])
 def test_tokens_whose_queries_have_an_outlier(n, d, bits):
     """One element of each query is 2^bits where the keys are zeros: the scores come from the others, in full."""
@@ -602,5 +602,22 @@ def test_tokens_with_large_queries_over_large_keys_that_do_not_meet(n):
         return q
     s, q, keep, out, lse = wide_scale_tokens(change, n, q=query)
     o, l, oe, le = ref.attention(q, *s.held(), keep, 2.0 ** -20)
+    ref.check(out, o, oe, "out")
+    ref.check(lse, l, le, "lse")
+
+
+@pytest.mark.parametrize("heads,n", [(13, 8), (13, 7), (12, 8), (11, 8), (11, 9), (2, 47), (2, 48), (1, 95), (1, 96)])
+@pytest.mark.parametrize("d,flags", [(64, N_), (128, N_ | D_ | B_)])
+def test_tokens_on_both_sides_of_grouping(heads, n, d, flags):
+    """8 tokens and 96 (token, head) pairs, one less of either, scattered over the clip."""
+    s = Setup(4, 11, 19, heads, d, 0.85, 2, flags)
+    s.store()
+    g = torch.Generator(device="cuda").manual_seed(n)
+    token = torch.randint(0, s.i.N, (n,), generator=g, device="cuda", dtype=torch.int32)
+    radius = torch.randint(-1, 20, (heads, n), generator=g, device="cuda", dtype=torch.int32)
+    out, lse = s.tokens(token, radius, 4)
+    s.ok()
+    keep = ref.pairs_kept(4, 11, 19, 0.85, 2, token.long(), torch.arange(s.i.N, device="cuda"), radius, bool(flags & D_))
+    o, l, oe, le = ref.attention(s.q[:, token.long()], *s.held(), keep, 2.0 ** -20)
     ref.check(out, o, oe, "out")
     ref.check(lse, l, le, "lse")
