@@ -103,19 +103,45 @@ bool take_error_word(unsigned int& word)
     return true;
 }
 
+// An identity of the current CUDA context that no other context of the process
+// shares, not even the one that takes its place after cudaDeviceReset; 0 where
+// it cannot be told.
+uint64_t context_id()
+{
+    using GetCurrent = CUresult (*)(CUcontext*);
+    using GetId = CUresult (*)(CUcontext, unsigned long long*);
+    static GetCurrent get_current = nullptr;
+    static GetId get_id = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *a = nullptr, *b = nullptr;
+        cudaDriverEntryPointQueryResult qa, qb;
+        if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &a, cudaEnableDefault, &qa) == cudaSuccess &&
+            cudaGetDriverEntryPoint("cuCtxGetId", &b, cudaEnableDefault, &qb) == cudaSuccess &&
+            qa == cudaDriverEntryPointSuccess && qb == cudaDriverEntryPointSuccess) {
+            get_current = reinterpret_cast<GetCurrent>(a);
+            get_id = reinterpret_cast<GetId>(b);
+        }
+    });
+    CUcontext ctx = nullptr;
+    unsigned long long id = 0;
+    if (!get_id || get_current(&ctx) != CUDA_SUCCESS || !ctx || get_id(ctx, &id) != CUDA_SUCCESS) return 0;
+    return id + 1;
+}
+
 // Lets KERNEL (no static shared memory) use all of a CTA's shared memory, once
-// per device: the attribute outlives the call, and setting it costs about as
-// much as a launch.
+// per context: the attribute lives as long as the context, and setting it
+// costs about as much as a launch.
 template <auto KERNEL>
 bool allow_max_smem()
 {
-    static std::atomic<uint64_t> done{0};
+    static std::atomic<uint64_t> done[64];                   // by device: the context it was last set in
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
-    if (done.load(std::memory_order_relaxed) & bit) return true;
+    const uint64_t ctx = dev < 64 ? context_id() : 0;
+    if (ctx && done[dev].load(std::memory_order_relaxed) == ctx) return true;
     if (!set_smem(KERNEL, kMaxSmem)) return false;
-    done.fetch_or(bit, std::memory_order_relaxed);
+    if (ctx) done[dev].store(ctx, std::memory_order_relaxed);
     return true;
 }
 
