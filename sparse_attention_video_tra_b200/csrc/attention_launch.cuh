@@ -29,7 +29,7 @@ tra_status launch_attention(const tra::Geom& G, const CUtensorMap& q, const CUte
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, kern, q, k, v, G, mask, out, qraw, lse, span) != cudaSuccess) return TRA_ERR_CUDA;
+        if (!cuda_ok(cudaLaunchKernelEx(&cfg, kern, q, k, v, G, mask, out, qraw, lse, span))) return TRA_ERR_CUDA;
     } else {
         kern<<<dim3(ctas, G.G), C::THREADS, smem, st>>>(q, k, v, G, mask, out, qraw, lse, span);
     }

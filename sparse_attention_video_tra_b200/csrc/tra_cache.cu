@@ -165,11 +165,11 @@ extern "C" tra_status tra_cache_attention_tokens(tra_plan plan, const void* q, c
     cfg.dynamicSmemBytes = !grouped ? 0 : G.D == 64 ? tra::group_smem_bytes<64>() : tra::group_smem_bytes<128>();
     auto go = [&](auto one, auto many) {
         if (grouped && !set_smem(many, (int)cfg.dynamicSmemBytes)) return false;
-        if (csize > 8 && cudaFuncSetAttribute(one, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
-        return (grouped ? cudaLaunchKernelEx(&cfg, many, G, cache_view(G, cache), (const uint32_t*)q, token, radius, n,
-                                             cached_frames, csize, out, bf16, lse)
-                        : cudaLaunchKernelEx(&cfg, one, G, cache_view(G, cache), (const uint4*)q, token, radius, n,
-                                             cached_frames, csize, out, bf16, lse)) == cudaSuccess;
+        if (csize > 8 && !cuda_ok(cudaFuncSetAttribute(one, cudaFuncAttributeNonPortableClusterSizeAllowed, 1))) return false;
+        return cuda_ok(grouped ? cudaLaunchKernelEx(&cfg, many, G, cache_view(G, cache), (const uint32_t*)q, token, radius, n,
+                                                    cached_frames, csize, out, bf16, lse)
+                               : cudaLaunchKernelEx(&cfg, one, G, cache_view(G, cache), (const uint4*)q, token, radius, n,
+                                                    cached_frames, csize, out, bf16, lse));
     };
     bool ok;
     if (G.D == 64) ok = G.disk ? go(tra::token_attention_kernel<64, true>, tra::token_group_kernel<64, true>)

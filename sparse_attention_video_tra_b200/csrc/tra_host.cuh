@@ -18,6 +18,15 @@
 
 namespace {
 
+// True if a runtime call succeeded.  An error is taken off the runtime's record,
+// where launch_status() of the next call would find it.
+bool cuda_ok(cudaError_t e)
+{
+    if (e == cudaSuccess) return true;
+    cudaGetLastError();
+    return false;
+}
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -29,7 +38,7 @@ EncodeTiledFn encode_fn()
     std::call_once(once, [] {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        if (cuda_ok(cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q)) &&
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<EncodeTiledFn>(p);
     });
@@ -81,7 +90,7 @@ tra_status launch_status()
 template <class K>
 bool set_smem(K kernel, int bytes)
 {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+    return cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
 }
 
 // streaming multiprocessors of the card
@@ -94,10 +103,10 @@ constexpr int kMaxSmem = 232448;
 bool take_error_word(unsigned int& word)
 {
     unsigned int w = 0;
-    if (cudaMemcpyFromSymbol(&w, tra::g_tra_error, sizeof w) != cudaSuccess) return false;
+    if (!cuda_ok(cudaMemcpyFromSymbol(&w, tra::g_tra_error, sizeof w))) return false;
     if (w) {
         const unsigned int zero = 0;
-        if (cudaMemcpyToSymbol(tra::g_tra_error, &zero, sizeof zero) != cudaSuccess) return false;
+        if (!cuda_ok(cudaMemcpyToSymbol(tra::g_tra_error, &zero, sizeof zero))) return false;
     }
     word |= w;
     return true;
@@ -116,8 +125,8 @@ uint64_t context_id()
     std::call_once(once, [] {
         void *a = nullptr, *b = nullptr;
         cudaDriverEntryPointQueryResult qa, qb;
-        if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &a, cudaEnableDefault, &qa) == cudaSuccess &&
-            cudaGetDriverEntryPoint("cuCtxGetId", &b, cudaEnableDefault, &qb) == cudaSuccess &&
+        if (cuda_ok(cudaGetDriverEntryPoint("cuCtxGetCurrent", &a, cudaEnableDefault, &qa)) &&
+            cuda_ok(cudaGetDriverEntryPoint("cuCtxGetId", &b, cudaEnableDefault, &qb)) &&
             qa == cudaDriverEntryPointSuccess && qb == cudaDriverEntryPointSuccess) {
             get_current = reinterpret_cast<GetCurrent>(a);
             get_id = reinterpret_cast<GetId>(b);
@@ -137,7 +146,7 @@ bool allow_max_smem()
 {
     static std::atomic<uint64_t> done[64];                   // by device: the context it was last set in
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (!cuda_ok(cudaGetDevice(&dev))) return false;
     const uint64_t ctx = dev < 64 ? context_id() : 0;
     if (ctx && done[dev].load(std::memory_order_relaxed) == ctx) return true;
     if (!set_smem(KERNEL, kMaxSmem)) return false;
