@@ -353,7 +353,8 @@ TRA_API tra_status tra_cache_attention_bytes(tra_plan plan, int n_frames, size_t
 /*
  * tra_cache_attention_tokens -- the same for n single tokens, each with its own
  * radius instead of a mask buffer.
- *   q        device bf16 [heads][n][d], 16-byte aligned
+ *   q        device bf16 [heads][n][d], 16-byte aligned; finite, magnitudes below
+ *            2^112 (its products with codes of up to 448 are fp32)
  *   token    device int32 [n], the natural index (t*H + h)*W + w of each token
  *            (any order, repeats allowed).  A negative index marks an unused
  *            place: its rows of out and lse are left as they were.  An index of

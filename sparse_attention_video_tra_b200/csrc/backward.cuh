@@ -971,8 +971,10 @@ __device__ __forceinline__ void backward_q(uint8_t* smem, const CUtensorMap& tm_
 }
 
 // Both in one launch, the longer key tiles (z = 0) first: neither needs the other,
-// a small grid fills the SMs with both at once (5 x 17 x 23, 3 heads: 75 CTAs
-// each), and the query slots fill the tail of the key tiles.
+// a small grid has more CTAs to run at once, and the query slots fill the tail of
+// the key tiles.  A grid of little more CTAs than SMs pays for the last ones: at
+// 5 x 17 x 23, 3 heads, two of 150 CTAs, query slots, start only when another slot
+// has ended, and two slots in a row outlast one key tile.
 // Tensor-bound on the tiles it computes: at 21 x 45 x 80, 4 heads, d = 128, sorted
 // groups, 462 241 tile pairs of 7 products take 10.3 ms, 1.32 PFLOP/s (0.94 of
 // what a plain bf16 product sustains on this card); one part alone takes 3280

@@ -401,12 +401,12 @@ token_attention_kernel(const Geom G, const CacheView C, const uint4* __restrict_
 //               pair of keys is one byte permute of two words.  The weight of a
 //               code, P times the V scale, is split into three bf16 parts: 24
 //               bits over fp32's whole range, so tiles of any scales may meet
-//               in a row (two f16 parts in a frame that follows the scales cost
-//               an eighth less time, but lose the tiles far below it).
+//               in a row (two f16 parts in a frame that follows the scales take
+//               6 to 9 % less time, but lose the tiles far below it).
 // Both products run in bf16: it holds every code, and Q as it comes.  (f16 takes
-// two instructions less per pair of codes, a twentieth of the time, but there a
-// Q row has to be scaled to f16's range, and its elements 2^33 below the largest
-// one are lost beside it, also where that one meets keys of zero.)
+// three instructions less per pair of codes, 1 to 5 % of the time, but there a Q
+// row has to be scaled to f16's range, and its elements 2^33 below the largest
+// one lose their bits beside it, also where that one meets keys of zero.)
 __device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t x)      // codes in bytes 0 and 1; exact
 {
     uint32_t r;

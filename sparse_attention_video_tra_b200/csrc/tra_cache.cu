@@ -139,8 +139,8 @@ extern "C" tra_status tra_cache_attention_tokens(tra_plan plan, const void* q, c
     const long long work = grouped ? (long long)((n + tra::GROUP - 1) / tra::GROUP) * G.G : units;
     // CTAs per group or token and head, a cluster.  Groups run one CTA per SM: the
     // most that all run at once, counting that a cluster lies within one GPC and
-    // large ones leave SMs over (24 clusters of 5: 41 us, of 6: 59 us; 48 of
-    // 3: 65 us, of 4: 72 us).  Lone tokens: as many as stay resident together, 16
+    // large ones leave SMs over (24 clusters of 5: 46 us, of 6: 56 us; 48 of
+    // 3: 73 us, of 4: 81 us).  Lone tokens: as many as stay resident together, 16
     // (a quarter faster for 1 token and 12 heads) while they cost no other its place.
     int csize = 8;
     if (grouped) {
