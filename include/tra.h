@@ -258,7 +258,7 @@ TRA_API tra_status tra_attention(tra_plan plan, const void* q, const void* k, co
  * differ by the rounding of P.
  *   q, k, v, mask, out   as tra_attention
  *   lse   device fp32 [heads][N_pad] ([heads][N] with TRA_FLAG_NATURAL); pad
- *         rows unspecified
+ *         rows unspecified; NaN where a kept score is NaN
  * Asynchronous on `stream`.
  */
 TRA_API tra_status tra_attention_lse(tra_plan plan, const void* q, const void* k, const void* v,

@@ -808,7 +808,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 else
                     reinterpret_cast<float4*>(static_cast<float*>(out) + orow * D)[ch] =
                         make_float4(oj.x * inv, oj.y * inv, oj.z * inv, oj.w * inv);
-                if (ch == 0) lse[orow] = lj > 0.f ? (mj + log2f(lj)) * 0.69314718055994531f : -INFINITY;
+                if (ch == 0) lse[orow] = lj == 0.f ? -INFINITY : (mj + log2f(lj)) * 0.69314718055994531f;
             }
             cluster_sync();                                 // the others' shared memory stays until it has been read
         } else if (ok && (k > 0 || (SPAN && active))) {
@@ -820,7 +820,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const bool store = !G.natural || qvalid;          // natural layout has no pad rows
                 const size_t orow = query_row(tq, hq, wq, qt * 128 + qrow) * D;
                 if constexpr (LSE) {
-                    if (store) lse[orow / D] = l > 0.f ? (m_run + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                    if (store) lse[orow / D] = l == 0.f ? -INFINITY : (m_run + log2f(l)) * 0.69314718055994531f;
                 }
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {

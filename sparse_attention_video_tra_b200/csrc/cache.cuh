@@ -368,16 +368,16 @@ token_attention_kernel(const Geom G, const CacheView C, const uint4* __restrict_
             const float* ml = csize > 1 ? cluster.map_shared_rank(s_ml, c) : s_ml;
             const float* os = csize > 1 ? cluster.map_shared_rank(s_out, c) : s_out;
             const float mo = ml[0];
-            if (mo == -INFINITY) continue;
+            if (ml[1] == 0.f) continue;                      // kept no key; a NaN stays one
             const float mn = fmaxf(mc, mo), a = ex2(mc - mn), b = ex2(mo - mn);
             lc = lc * a + ml[1] * b;
             oc = oc * a + os[tid] * b;
             mc = mn;
         }
-        const float val = lc > 0.f ? oc / lc : 0.f;
+        const float val = lc == 0.f ? 0.f : oc / lc;
         if (out_bf16) static_cast<__nv_bfloat16*>(out)[row * D + tid] = __float2bfloat16(val);
         else static_cast<float*>(out)[row * D + tid] = val;
-        if (tid == 0) lse[row] = lc > 0.f ? (mc + log2f(lc)) * 0.69314718055994531f : -INFINITY;
+        if (tid == 0) lse[row] = lc == 0.f ? -INFINITY : (mc + log2f(lc)) * 0.69314718055994531f;
     }
     if (csize > 1) cluster.sync();                           // the others' shared memory stays until it has been read
 }
@@ -748,16 +748,16 @@ token_group_kernel(const Geom G, const CacheView C, const uint32_t* __restrict__
                 const float* ml = csize > 1 ? cluster.map_shared_rank(&s_ml[r][0], k) : &s_ml[r][0];
                 const float* os = csize > 1 ? cluster.map_shared_rank(&s_o[0][r][0], k) : &s_o[0][r][0];
                 const float mo = ml[0];
-                if (mo == -INFINITY) continue;
+                if (ml[1] == 0.f) continue;                  // kept no key; a NaN stays one
                 const float mn = fmaxf(mc, mo), a = ex2(mc - mn), b = ex2(mo - mn);
                 lc = lc * a + ml[1] * b;
                 oc = oc * a + os[d] * b;
                 mc = mn;
             }
-            const float val = lc > 0.f ? oc / lc : 0.f;
+            const float val = lc == 0.f ? 0.f : oc / lc;
             if (out_bf16) static_cast<__nv_bfloat16*>(out)[row * D + d] = __float2bfloat16(val);
             else static_cast<float*>(out)[row * D + d] = val;
-            if (d == 0) lse[row] = lc > 0.f ? (mc + log2f(lc)) * 0.69314718055994531f : -INFINITY;
+            if (d == 0) lse[row] = lc == 0.f ? -INFINITY : (mc + log2f(lc)) * 0.69314718055994531f;
         }
     }
     if (csize > 1) cluster.sync();                           // the others' shared memory stays until it has been read

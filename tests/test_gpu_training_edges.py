@@ -226,3 +226,61 @@ def test_corrupted_masks_in_every_form_of_the_forward(grid, flags):
             assert c.plan.status() == 0
             for x, y in zip(want, again):
                 assert torch.equal(x, y)
+
+
+def same_but_nan(got, want, bad):
+    """NaN in the rows of `bad`, the bits of want elsewhere."""
+    assert torch.isnan(got[bad]).all()
+    assert torch.equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("grid", [(5, 8, 8, 2, 64, 0.7, 1), (5, 17, 23, 2, 128, 0.8, 3), (5, 17, 23, 8, 128, 0.8, 3)])
+def test_a_nan_query_gives_nan_rows_not_empty_ones(grid):
+    """In every form of the forward, over the cache too: out and lse of that row are NaN, the other rows as they were."""
+    c = Case(*grid, N_)
+    q, k, v = c.nat
+    cache = c.plan.new_cache()
+    c.plan.cache_store(k, v, 0, cache)
+    ws = c.plan.new_cache_workspace(grid[0])
+    bad = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    bad[0, 3] = bad[-1, -1] = True
+    spoilt = q.clone()
+    spoilt[bad] = float("nan")
+
+    def lse_call(q, out, lse):
+        c.plan.attention_lse(q, k, v, c.mask, out, lse)
+
+    def frames_call(q, out, lse):
+        c.plan.cache_attention(q, 0, cache, grid[0], c.mask, out, lse, ws)
+
+    for call in (lse_call, frames_call):
+        res = []
+        for x in (q, spoilt):
+            out, lse = c.plan.new_out(), c.plan.new_lse()
+            call(x, out, lse)
+            res.append((out, lse))
+        c.ok()
+        same_but_nan(res[1][0], res[0][0], bad)
+        same_but_nan(res[1][1], res[0][1], bad)
+
+
+@pytest.mark.parametrize("n", [3, 7, 40])
+def test_a_nan_query_of_a_token_gives_nan_not_an_empty_row(n):
+    c = Case(5, 17, 23, 3, 128, 0.8, 3, N_)
+    cache = c.plan.new_cache()
+    c.plan.cache_store(c.nat[1], c.nat[2], 0, cache)
+    token = torch.arange(800, 800 + n, device="cuda", dtype=torch.int32)
+    radius = torch.full((3, n), 4, device="cuda", dtype=torch.int32)
+    bad = torch.zeros(3, n, dtype=torch.bool, device="cuda")
+    bad[1, n // 2] = bad[2, 0] = True
+    radius[2, 1] = -1                                    # an empty row stays one
+    q = c.nat[0][:, token.long()].contiguous()
+    res = []
+    for x in (q, q.masked_fill(bad[..., None], float("nan"))):
+        out, lse = torch.empty(3, n, 128, device="cuda"), torch.empty(3, n, device="cuda")
+        c.plan.cache_attention_tokens(x, token, radius, cache, 5, out, lse)
+        res.append((out, lse))
+    c.ok()
+    same_but_nan(res[1][0], res[0][0], bad)
+    same_but_nan(res[1][1], res[0][1], bad)
+    assert torch.isneginf(res[1][1][2, 1]) and not res[1][0][2, 1].any()
