@@ -366,7 +366,7 @@ TRA_API tra_status tra_cache_attention_bytes(tra_plan plan, int n_frames, size_t
  *   lse      device fp32 [heads][n]; zeros and -infinity where no cached key
  *            is kept
  * n = 0 does nothing.  To fp32 accuracy: scores and sums are fp32, and where many
- * tokens run on the tensor cores the weights of v are three bf16 parts each.
+ * tokens run on the tensor cores the probabilities are three bf16 parts each.
  * Asynchronous on `stream`.
  */
 TRA_API tra_status tra_cache_attention_tokens(tra_plan plan, const void* q, const int32_t* token,

@@ -398,11 +398,11 @@ token_attention_kernel(const Geom G, const CacheView C, const uint4* __restrict_
 //   softmax     running maximum and sum of the unrounded P per row, in fp32
 //   O += P V    d/8 column tiles.  Column n of tile j is the d element
 //               (d/8) n + j, so the lane needs byte j of four key rows, and each
-//               pair of keys is one byte permute of two words.  The weight of a
-//               code, P times the V scale, is split into three bf16 parts: 24
-//               bits over fp32's whole range, so tiles of any scales may meet
-//               in a row (two f16 parts in a frame that follows the scales take
-//               6 to 9 % less time, but lose the tiles far below it).
+//               pair of keys is one byte permute of two words.  P is split into
+//               three bf16 parts, 24 bits over the whole range of P (two f16
+//               parts take a tenth less time, but their range is 2^40), and
+//               the granule's sum joins O times its V scale in fp32, so tiles
+//               of any scales may meet in a row.
 // Both products run in bf16: it holds every code, and Q as it comes.  (f16 takes
 // three instructions less per pair of codes, 1 to 5 % of the time, but there a Q
 // row has to be scaled to f16's range, and its elements 2^33 below the largest
@@ -421,6 +421,14 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// the same from zeros
+__device__ __forceinline__ void mma_bf16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 struct GranuleFrame {
@@ -655,7 +663,7 @@ token_group_kernel(const Geom G, const CacheView C, const uint32_t* __restrict__
                 mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
                 mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
             }
-            uint32_t ph[4], pm[4], pl[4];                    // the weights' parts
+            uint32_t ph[4], pm[4], pl[4];                    // the parts of P
             float al[2] = {1.f, 1.f};
             bool raise = false;
 #pragma unroll
@@ -671,9 +679,8 @@ token_group_kernel(const Geom G, const CacheView C, const uint32_t* __restrict__
                 for (int j = 0; j < 2; ++j) {
                     const float a = ex2(p[x][2 * j] - base), b = ex2(p[x][2 * j + 1] - base);
                     l[x] += a + b;
-                    const float av = a * vs, bv = b * vs;
-                    const uint32_t hi = pack_bf16x2(av, bv);
-                    const float ar = av - __uint_as_float(hi << 16), br = bv - __uint_as_float(hi & 0xffff0000u);
+                    const uint32_t hi = pack_bf16x2(a, b);
+                    const float ar = a - __uint_as_float(hi << 16), br = b - __uint_as_float(hi & 0xffff0000u);
                     const uint32_t mid = pack_bf16x2(ar, br);
                     ph[2 * j + x] = hi;
                     pm[2 * j + x] = mid;
@@ -695,9 +702,12 @@ token_group_kernel(const Geom G, const CacheView C, const uint32_t* __restrict__
                 const uint32_t sel = (uint32_t)((j & 3) | ((4 + (j & 3)) << 4));
                 const uint32_t b0 = codes_to_bf16x2(__byte_perm(vv[0][j >> 2], vv[1][j >> 2], sel));
                 const uint32_t b1 = codes_to_bf16x2(__byte_perm(vv[2][j >> 2], vv[3][j >> 2], sel));
-                mma_bf16(o[j], pl, b0, b1);
-                mma_bf16(o[j], pm, b0, b1);
-                mma_bf16(o[j], ph, b0, b1);
+                float pv[4];
+                mma_bf16_first(pv, pl, b0, b1);
+                mma_bf16(pv, pm, b0, b1);
+                mma_bf16(pv, ph, b0, b1);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[j][k] = fmaf(vs, pv[k], o[j][k]);
             }
         }
     }

@@ -127,20 +127,20 @@ extern "C" tra_status tra_cache_attention_tokens(tra_plan plan, const void* q, c
     // Groups of 16 tokens share a key's codes on the tensor cores once enough of a
     // group's rows are filled and there is work for the card; below, one token at
     // a time over more CTAs.  Measured cold on neighbouring tokens, one token at a
-    // time / grouped: with 40 heads at 21 x 45 x 80 88 / 94 us for 6 tokens,
-    // 168 / 102 for 8 and 154 / 102 for 16; with 12 heads at 21 x 30 x 52 31 / 29 us
-    // for 8 and 47 / 33 for 16.  With few heads: 4 at 21 x 45 x 80 41 / 49 us for 16,
-    // 49 / 49 for 24, 61 / 45 for 48; 2 at 21 x 30 x 52 25 / 31 us for 32, 31 / 33 for
-    // 48, 29 / 29 for 64; 4 at 9 x 17 x 23 16 / 16 us for 8 to 32, 20 / 18 for 64.
+    // time / grouped: with 40 heads at 21 x 45 x 80 86 / 98 us for 6 tokens,
+    // 169 / 109 for 8 and 160 / 110 for 16; with 12 heads at 21 x 30 x 52 33 / 30 us
+    // for 8 and 49 / 35 for 16.  With few heads: 4 at 21 x 45 x 80 43 / 51 us for 16,
+    // 50 / 51 for 24, 62 / 48 for 48; 2 at 21 x 30 x 52 26 / 31 us for 32, 33 / 35 for
+    // 48, 31 / 31 for 64; 4 at 9 x 17 x 23 18 / 18 us for 16 to 32, 22 / 20 for 64.
     // (Tokens scattered over the clip share few keys and are faster one at a time,
-    // 162 against 283 us for 64 of 12 heads, but where they lie is known on the
+    // 168 against 293 us for 64 of 12 heads, but where they lie is known on the
     // device only.)
     const bool grouped = n >= 8 && units >= 96;
     const long long work = grouped ? (long long)((n + tra::GROUP - 1) / tra::GROUP) * G.G : units;
     // CTAs per group or token and head, a cluster.  Groups run one CTA per SM: the
     // most that all run at once, counting that a cluster lies within one GPC and
-    // large ones leave SMs over (24 clusters of 5: 46 us, of 6: 56 us; 48 of
-    // 3: 73 us, of 4: 81 us).  Lone tokens: as many as stay resident together, 16
+    // large ones leave SMs over (24 clusters of 5: 47 us, of 6: 57 us; 48 of
+    // 3: 74 us, of 4: 82 us).  Lone tokens: as many as stay resident together, 16
     // (a quarter faster for 1 token and 12 heads) while they cost no other its place.
     int csize = 8;
     if (grouped) {

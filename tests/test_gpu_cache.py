@@ -621,3 +621,17 @@ def test_tokens_on_both_sides_of_grouping(heads, n, d, flags):
     o, l, oe, le = ref.attention(s.q[:, token.long()], *s.held(), keep, 2.0 ** -20)
     ref.check(out, o, oe, "out")
     ref.check(lse, l, le, "lse")
+
+
+@pytest.mark.parametrize("n,d", [(5, 128), (8, 128), (52, 128), (16, 64)])
+@pytest.mark.parametrize("bits", [-100, -110, -116, 100, 116])
+def test_tokens_over_the_smallest_and_largest_values(n, d, bits):
+    """Values near the ends of the type's exponents keep as many bits as ordinary ones (compared after a power of two)."""
+    def change(s):
+        s.v.mul_(2.0 ** bits)
+    s, q, keep, out, lse = wide_scale_tokens(change, n, d)
+    k, v = s.held()
+    o, l, oe, le = ref.attention(q, k, v * 2.0 ** -bits, keep, 2.0 ** -20)
+    assert out.dtype == torch.float32
+    ref.check(out * 2.0 ** -bits, o, oe, "out")
+    ref.check(lse, l, le, "lse")
